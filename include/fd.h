@@ -379,6 +379,8 @@ unsigned fd_get_launch_flags(void);
  * fails. Not capturable in a CUDA graph (it synchronises).
  */
 #define FD_DEVICE_STATUS_WAIT_TIMEOUT 1u
+/* a page number that a call needed was outside the cache (fd_paged_batch) */
+#define FD_DEVICE_STATUS_BAD_PAGE 2u
 int fd_device_status(fd_stream_t stream, unsigned *status, int clear);
 
 /*
@@ -436,6 +438,149 @@ int fd_nvfp4_scaled_mm(const void *x, const void *x_sf, const void *w, const voi
  * Returns FD_ERR_UNSUPPORTED when the kernel has no plan for the shape.
  */
 int fd_debug_plan_nvfp4(int M, int K, int N, int smem_budget, int *plan);
+
+/*
+ * ---------------------------------------------------------------- the attention half
+ * Rotary positions, the paged key/value cache and the attention over it: what lies between
+ * the QKV product of a decode layer and its output projection.
+ *
+ * fd_heads - a bf16 activation of `heads` heads per token: element (t, h, j) is
+ * data[t * token_stride + h * head_stride + j], j < head_dim. Strides are in elements, not
+ * negative and multiples of 8; an input may be a view of a wider row (the q, k and v parts of
+ * one QKV row). An output's elements must not overlap one another (FD_ERR_OVERLAP).
+ */
+typedef struct fd_heads {
+    void *data;
+    long long token_stride;
+    long long head_stride;
+    int heads;
+} fd_heads;
+
+/*
+ * fd_paged_cache - keys and values of many sequences in pages of page_size tokens. Element
+ * (page, token, head, j) of the keys is k[page * k_page_stride + token * k_token_stride +
+ * head * k_head_stride + j], of the values likewise with the v_ strides: tokens before heads,
+ * heads before tokens, or keys and values in one buffer are all strides. In elements; where the
+ * dimension has more than one entry, a positive multiple of 8, and each stride a multiple of
+ * every smaller one (which every packed layout is).
+ * page_size  a power of two, 16 .. FD_MAX_PAGE_SIZE.   head_dim  64 or 128.
+ */
+typedef struct fd_paged_cache {
+    void *k;
+    void *v;
+    long long k_page_stride, k_token_stride, k_head_stride;
+    long long v_page_stride, v_token_stride, v_head_stride;
+    int num_pages;
+    int page_size;
+    int kv_heads;
+    int head_dim;
+} fd_paged_cache;
+
+/*
+ * fd_paged_batch - which tokens belong to which sequence, and where its keys are. All three
+ * arrays are DEVICE memory, read when the kernel runs (a captured graph may be replayed with
+ * new contents), 4-byte aligned.
+ * q_start      int32 [batch + 1], ascending from 0: the new tokens of sequence b are the rows
+ *              q_start[b] .. q_start[b + 1] - 1 of the activations (none is allowed). Rows from
+ *              q_start[batch] on belong to no sequence and are left as they were.
+ * kv_len       int32 [batch]: tokens in the sequence's cache, the new ones included; new token i
+ *              of q_len is number kv_len - q_len + i.
+ * block_table  int32 [batch, table_stride]: entry j of a row is the page of the tokens
+ *              j * page_size .. . Entries past the last page that a call needs are not read.
+ * total_q      rows of the activations; max_q: no sequence has more new tokens (rows past it are
+ *              not computed); max_pages: entries of a table row; a kv_len above
+ *              max_pages * page_size counts as that.
+ * An entry outside 0 .. num_pages - 1 in a place that is needed sets FD_DEVICE_STATUS_BAD_PAGE:
+ * its keys and values read as zeros, and nothing is written to it.
+ */
+typedef struct fd_paged_batch {
+    const int *q_start;
+    const int *kv_len;
+    const int *block_table;
+    int table_stride;
+    int batch;
+    int total_q;
+    int max_q;
+    int max_pages;
+} fd_paged_batch;
+
+#define FD_MAX_PAGE_SIZE 1024
+#define FD_MAX_BATCH 4096         /* sequences of one fd_paged_batch */
+#define FD_MAX_HEADS 1024         /* heads of one fd_heads */
+#define FD_MAX_ROPE_DIM 256       /* head_dim of fd_rope */
+#define FD_MAX_SEQ 16777216       /* max_pages * page_size */
+
+/*
+ * fd_rope - rotary positions on queries and keys.
+ *   a        = positions[t] * inv_freq[i],                        i < rot_dim / 2
+ *   y[p0(i)] = bf16( scale * (x[p0(i)] cos a - x[p1(i)] sin a) )
+ *   y[p1(i)] = bf16( scale * (x[p0(i)] sin a + x[p1(i)] cos a) )
+ *   y[j]     = x[j]                                               j >= rot_dim
+ * interleaved 0: p0 = i, p1 = i + rot_dim / 2 (the two halves of the rotated part);
+ * interleaved 1: p0 = 2 i, p1 = 2 i + 1.
+ * inv_freq  fp64 [rot_dim / 2] in device memory, 8-byte aligned: any stretching of the positions
+ *           for long contexts is in it (rope_inv_freq of the Python package makes the usual
+ *           ones), `scale` is the factor on cosine and sine that goes with it (1 for none).
+ * positions int32 [tokens]; any value. The angle is reduced to one turn in 64-bit fixed point, so
+ *           it is as exact at position 2^31 as at 0 (its error is below 1e-6 radians).
+ * q, k      inputs; k and k_out may both be NULL (queries alone). q_out, k_out: outputs; each may
+ *           be its input (same pointer and strides, in place), any other overlap with an input
+ *           or output is FD_ERR_OVERLAP.
+ * Requires  tokens >= 0, head_dim a multiple of 8 up to FD_MAX_ROPE_DIM, rot_dim even,
+ *           2 <= rot_dim <= head_dim, scale finite, heads of an output equal to its input's.
+ *           tokens == 0 is an empty call: FD_OK at once, no pointer read, nothing launched.
+ */
+int fd_rope(const fd_heads *q, const fd_heads *k, const fd_heads *q_out, const fd_heads *k_out,
+            const int *positions, const double *inv_freq, int tokens, int head_dim, int rot_dim,
+            int interleaved, float scale, fd_stream_t stream);
+
+/*
+ * fd_rope_append - fd_rope, with the rotated keys and the values written to their places in the
+ * cache instead of to a buffer: one pass over the QKV rows of a batch's new tokens.
+ * q, k, v    [total_q] tokens; k and v have cache->kv_heads heads. q_out as in fd_rope.
+ * positions  int32 [total_q], or NULL: the token's number in its cache.
+ * A token whose number is negative (kv_len below the number of new tokens: a padded sequence of
+ * a captured batch may have kv_len 0) has no place and is not written; one at or past
+ * max_pages * page_size is not written and sets FD_DEVICE_STATUS_BAD_PAGE. Two sequences must not
+ * write the same place of a shared page in one call. The cache may not overlap itself, q, k, v or
+ * q_out.
+ */
+int fd_rope_append(const fd_heads *q, const fd_heads *k, const fd_heads *v, const fd_heads *q_out,
+                   const fd_paged_cache *cache, const fd_paged_batch *batch, const int *positions,
+                   const double *inv_freq, int rot_dim, int interleaved, float scale,
+                   fd_stream_t stream);
+
+/*
+ * fd_paged_attention - attention of each sequence's new tokens over its cache, the new tokens'
+ * own keys included (fd_rope_append comes first): one token when decoding, a chunk of any
+ * length when a prompt is read, both in one batch.
+ *   s(i, j)  = scale * <q_i, k_j>;  softcap > 0: s = softcap * tanh(s / softcap)
+ *   visible  j < kv_len; causal: j <= p_i; window > 0: j > p_i - window;  p_i = kv_len - q_len + i
+ *   out_i    = sum_j exp(s(i, j)) v_j / sum_j exp(s(i, j))       over the visible j
+ *   lse_i    = ln sum_j exp(s(i, j))
+ * Query head h reads key head h / (q_heads / kv_heads). A row that sees no key (kv_len 0, or
+ * fewer keys than new tokens) gives zeros and lse = -infinity.
+ * q, out    [total_q] tokens of q heads; out must not overlap q or the cache.
+ * lse       fp32 [total_q, q_heads], 4-byte aligned, or NULL.
+ * scratch   device memory of at least fd_paged_attention_scratch_bytes(...) bytes, 16-byte
+ *           aligned, ZERO before its first use; every completed call leaves its counters zero
+ *           again. Calls that share a scratch must not run concurrently (one per stream; two
+ *           graphs that may run at the same time need one each).
+ * Keys past kv_len, and what else lies in their pages, may hold anything, NaN included. Keys and
+ * values below kv_len must be finite where a later token of the same call sees them.
+ * Scores and probabilities: fp32 scores, maximum, sum and accumulator; each probability is
+ * rounded to bf16 for its product with v; one rounding of the result.
+ * Requires  q_heads a multiple of kv_heads, scale finite, window >= 0, softcap >= 0 and finite.
+ *           total_q == 0 or batch == 0 is an empty call: FD_OK at once, no pointer read.
+ */
+int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_paged_batch *batch,
+                       const fd_heads *out, float *lse, float scale, int causal, int window,
+                       float softcap, void *scratch, size_t scratch_bytes, fd_stream_t stream);
+
+/* Bytes of scratch that suffice for every fd_paged_attention call whose batch, total_q, heads,
+ * head_dim and max_q are at most these (host only; 0 for a size that the call refuses). */
+size_t fd_paged_attention_scratch_bytes(int batch, int total_q, int q_heads, int kv_heads,
+                                        int head_dim, int max_q);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *fd_status_string(int status);

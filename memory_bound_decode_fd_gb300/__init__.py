@@ -13,12 +13,20 @@
 * ``decode_mlp_step``: L layers of the two, in stream order.
 * ``decode_mlp_step_persistent``: the same L layers as one persistent launch, bit-identical.
 
+* ``rope``: rotary positions on queries and keys (halves or interleaved pairs, part of the
+  head, stretched for long contexts with ``rope_inv_freq``).
+* ``rope_append``: the same, with the keys and the values written into a paged cache.
+* ``paged_attention``: the new tokens of a batch (one each when decoding, chunks of any length)
+  attend over their pages.
+
 The compute runs in ``libfd.so`` (C ABI in ``include/fd.h``); this package marshals
 PyTorch CUDA tensors into it. Build the library with ``build.build()``. There is no CPU
 fallback: calling a kernel without the library raises ``FdLibraryMissing``.
 """
 
 from ._lib import (  # noqa: F401
+    FD_DEVICE_STATUS_BAD_PAGE,
+    FD_DEVICE_STATUS_WAIT_TIMEOUT,
     FD_ERR_ALIGN,
     FD_ERR_CUDA,
     FD_ERR_NULL,
@@ -37,6 +45,12 @@ from ._lib import (  # noqa: F401
     status_string,
 )
 from ._lib import load as load_library  # noqa: F401
+from .attention import (  # noqa: F401
+    paged_attention,
+    paged_attention_scratch,
+    rope,
+    rope_append,
+)
 from .kernels import (  # noqa: F401
     GEMV_PATHS,
     add_rmsnorm,
@@ -60,6 +74,7 @@ from .kernels import (  # noqa: F401
     w4a16_gate_up_gemv,
 )
 from .packing import pack_int4  # noqa: F401
+from .rotary import ROPE_SCALINGS, rope_inv_freq  # noqa: F401
 from .traffic import (  # noqa: F401
     add_rmsnorm_bytes,
     decode_step_bytes,

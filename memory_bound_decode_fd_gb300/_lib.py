@@ -25,6 +25,7 @@ FD_LAUNCH_PDL = 1
 FD_LAUNCH_TEST_FAIL = 256
 FD_LAUNCH_TEST_WAIT_TIMEOUT = 512
 FD_DEVICE_STATUS_WAIT_TIMEOUT = 1
+FD_DEVICE_STATUS_BAD_PAGE = 2
 
 FD_MAX_K = 32768
 FD_MAX_M = 256
@@ -32,6 +33,11 @@ FD_MAX_HIDDEN = 32768
 FD_NVFP4_MAX_K = 16384
 FD_FOLD_SCRATCH_BYTES = 4096
 FD_STEP_MAX_LAYERS = 1024
+FD_MAX_PAGE_SIZE = 1024
+FD_MAX_BATCH = 4096
+FD_MAX_HEADS = 1024
+FD_MAX_ROPE_DIM = 256
+FD_MAX_SEQ = 16777216
 
 
 
@@ -64,6 +70,11 @@ SIGNATURES = {
     "fd_debug_plan_nvfp4": (_I, [_I, _I, _I, _I, _VP]),
     "fd_add_rmsnorm": (_I, [_VP, _VP, _VP, ctypes.c_float, _VP, _VP, _I, _I, _VP]),
     "fd_w4_dequant_debug": (_I, [_VP, _VP, _VP, _I, _I, _I, _VP]),
+    "fd_rope": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, ctypes.c_float, _VP]),
+    "fd_rope_append": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, ctypes.c_float, _VP]),
+    "fd_paged_attention": (_I, [_VP, _VP, _VP, _VP, _VP, ctypes.c_float, _I, _I, ctypes.c_float, _VP,
+                                ctypes.c_size_t, _VP]),
+    "fd_paged_attention_scratch_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
     "fd_status_string": (ctypes.c_char_p, [_I]),
     "fd_last_cuda_error": (_I, []),
     "fd_version": (_I, []),

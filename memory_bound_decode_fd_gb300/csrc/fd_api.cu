@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "fd_attn.h"
 #include "fd_copy.h"
 #include "fd_gemv_plan.h"
 #include "fd_gemv_tc_plan.h"
@@ -95,6 +96,9 @@ cudaError_t device_info(DeviceInfo *info) {
 }
 
 unsigned launch_flags() { return g_launch_flags.load(std::memory_order_relaxed); }
+
+int api_status(cudaError_t err) { return from_cuda(err); }
+bool api_launch_fails() { return fake_launch_failure(); }
 
 }  // namespace fd
 
@@ -524,22 +528,25 @@ int fd_decode_mlp_step(const fd_step_layer *layers, int n_layers, const void *x0
 int fd_device_status(fd_stream_t stream, unsigned *status, int clear) {
     if (!status) return FD_ERR_NULL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // one word per file with bounded waits; pinned so the copies are truly asynchronous
+    // one word per file that records failures; pinned so the copies are truly asynchronous
+    cudaError_t (*const readers[])(cudaStream_t, unsigned *, bool) = {
+        status_gemv_tma, status_gemv_tc, status_nvfp4, status_decode_step, status_rope,
+        status_attn_rows};
+    constexpr int kWords = sizeof(readers) / sizeof(readers[0]);
     static thread_local unsigned *words = nullptr;
     if (!words) {
-        cudaError_t err = cudaMallocHost(&words, 4 * sizeof(unsigned));
+        cudaError_t err = cudaMallocHost(&words, kWords * sizeof(unsigned));
         if (err != cudaSuccess) return from_cuda(err);
     }
-    cudaError_t (*const readers[4])(cudaStream_t, unsigned *, bool) = {
-        status_gemv_tma, status_gemv_tc, status_nvfp4, status_decode_step};
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kWords; ++i) {
         words[i] = 0;
         cudaError_t err = readers[i](st, &words[i], clear != 0);
         if (err != cudaSuccess) return from_cuda(err);
     }
     cudaError_t err = cudaStreamSynchronize(st);
     if (err != cudaSuccess) return from_cuda(err);
-    *status = words[0] | words[1] | words[2] | words[3];
+    *status = 0;
+    for (int i = 0; i < kWords; ++i) *status |= words[i];
     return FD_OK;
 }
 

@@ -1,0 +1,101 @@
+// fd_attn.h - what the rotary, cache and attention sources share: the device view of a paged
+// batch, the visible range of a row, and the launchers (see include/fd.h for the operators).
+#pragma once
+
+#include <cuda.h>  // CUtensorMap (type only)
+
+#include "fd_internal.h"
+
+namespace fd {
+
+// A bf16 [tokens, heads, head_dim] view: strides in elements.
+struct HeadsView {
+    uint16_t *p;
+    long long ts, hs;
+};
+
+// The paged batch as a kernel reads it.
+struct PagedMeta {
+    const int *q_start;
+    const int *kv_len;
+    const int *table;
+    int table_stride;
+    int batch;
+    int total_q;
+    int max_q;
+    int capacity;    // max_pages * page_size
+    int num_pages;
+    int page_shift;  // log2(page_size)
+};
+
+struct SeqInfo {
+    int q0;    // first activation row
+    int rows;  // new tokens that are computed
+    int kv;    // tokens in the cache
+    int base;  // number of new token 0 (negative where it has no place)
+};
+
+// Reads sequence b's entries. Whatever the arrays hold, the rows lie in [0, total_q) and the
+// tokens in [0, capacity].
+__device__ __forceinline__ SeqInfo load_seq(const PagedMeta &m, int b) {
+    int q0 = m.q_start[b], q1 = m.q_start[b + 1], kv = m.kv_len[b];
+    q0 = min(max(q0, 0), m.total_q);
+    q1 = min(max(q1, q0), m.total_q);
+    kv = min(max(kv, 0), m.capacity);
+    return {q0, min(q1 - q0, m.max_q), kv, kv - (q1 - q0)};
+}
+
+// Keys [lo, hi) that new token i sees; lo >= hi: none.
+__device__ __forceinline__ int key_hi(const SeqInfo &s, int i, int causal) {
+    return causal ? min(s.kv, s.base + i + 1) : s.kv;
+}
+__device__ __forceinline__ int key_lo(const SeqInfo &s, int i, int window) {
+    return window > 0 ? max(0, s.base + i - window + 1) : 0;
+}
+
+// Where a dimension of the cache lies in its tensor map (1 .. 3, dimension 0 is head_dim).
+struct MapOrder {
+    int tok, head, page;
+};
+
+struct AttnArgs {
+    PagedMeta m;
+    HeadsView q, out;
+    float *lse;       // [total_q, q_heads] or null
+    MapOrder ok, ov;
+    int q_heads, kv_heads, group, head_dim;
+    int causal, window;
+    float scale;      // multiplies q.k
+    float softcap;    // 0: none
+    unsigned *counters;  // one per CTA, zero between calls
+    float *partials;
+};
+
+constexpr int kAttnMaxCtas = 256;             // largest grid (counters in the scratch)
+constexpr int kAttnCounterBytes = 4 * 4096;   // the scratch begins with them
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---- attention of few rows per key head (fd_attn_rows.cu)
+constexpr int kRowsM = 16;      // query rows of one pass over the keys
+constexpr int kRowsTile = 64;   // keys of one pipeline stage
+// fp32 words of a partial result: 16 rows of head_dim, then (maximum, sum) of each
+__host__ __device__ constexpr int rows_slot_words(int d) { return kRowsM * (d + 2); }
+cudaError_t launch_attn_rows(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
+                             cudaStream_t stream);
+cudaError_t status_attn_rows(cudaStream_t stream, unsigned *out, bool clear);
+
+// ---- rotary positions (fd_rope.cu)
+struct RopeArgs {
+    HeadsView q, k, v, q_out, k_out, v_out;  // k_out / v_out: the cache with its token and head strides
+    long long k_page, v_page;                // page strides of the cache
+    const int *positions;
+    const double *inv_freq;
+    PagedMeta m;                             // the batch (append only)
+    int tokens, q_heads, k_heads, head_dim, rot_dim, interleaved;
+    float scale;
+};
+cudaError_t launch_rope(const RopeArgs &a, bool append, cudaStream_t stream);
+cudaError_t status_rope(cudaStream_t stream, unsigned *out, bool clear);
+
+}  // namespace fd

@@ -26,6 +26,11 @@ cudaError_t device_info(DeviceInfo *info);
 // Process-wide launch options (fd_set_launch_flags), FD_LAUNCH_* bits.
 unsigned launch_flags();
 
+// For entry points outside fd_api.cu: the fd_status of a CUDA result (recorded for
+// fd_last_cuda_error), and whether FD_LAUNCH_TEST_FAIL asks for a failed launch.
+int api_status(cudaError_t err);
+bool api_launch_fails();
+
 // Launches `kern` on `stream`; with FD_LAUNCH_PDL set the launch allows programmatic
 // dependent launch (the kernel may start while the previous kernel in the stream is
 // finishing; each kernel waits on griddepcontrol before it touches data that a previous

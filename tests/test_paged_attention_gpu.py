@@ -1,0 +1,213 @@
+"""Attention over a paged cache against a plain 64-bit computation: decoding, chunks, masks that
+leave rows empty, group sizes, layouts, NaN behind the last token, bad pages, graphs and streams."""
+
+import pytest
+import torch
+
+import memory_bound_decode_fd_gb300 as fd
+from attn_check import Batch, check_attention
+
+pytestmark = pytest.mark.gpu
+
+
+def run(b, scratch=None, out=None, with_lse=True, **kw):
+    n, h, d = b.q.shape
+    if scratch is None:
+        scratch = fd.paged_attention_scratch(len(b.q_lens), n, b.hq, b.hk, b.d, b.max_q)
+    if out is None:
+        out = torch.full((n, h, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n, h), 5.0, device="cuda") if with_lse else None
+    fd.paged_attention(b.q, *b.args(), b.max_q, scratch, out=out, lse=lse, **kw)
+    return out, lse
+
+
+def checked(b, **kw):
+    fd.device_status()
+    scratch = fd.paged_attention_scratch(len(b.q_lens), b.q.shape[0], b.hq, b.hk, b.d, b.max_q)
+    out, lse = run(b, scratch, **kw)
+    assert fd.device_status() == 0
+    args = {"cap" if k == "softcap" else k: v for k, v in kw.items()}
+    check_attention(b, out, lse, **args)
+    n = sum(b.q_lens)  # rows behind the last sequence stay as they were
+    assert bool((out[n:] == 5.0).all()) and bool((lse[n:] == 5.0).all())
+    assert not scratch[:16384].any()  # counters are zero again
+    again, lse2 = run(b, scratch, **kw)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+
+
+DECODE = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 1000]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(8, 2), (1, 1), (7, 1), (6, 2), (16, 1), (32, 1), (40, 2)])
+def test_decode_lengths(cuda_device, d, hq, hk):
+    checked(Batch(hq, hk, d, [1] * len(DECODE), DECODE, seed=hq, spare_rows=1))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 1024])
+@pytest.mark.parametrize("head_major,fused", [(False, False), (True, False), (False, True), (True, True)])
+def test_page_sizes_and_layouts(cuda_device, page, head_major, fused):
+    checked(Batch(4, 2, 128, [1, 3, 70], [1030, 200, 1025], page, head_major, seed=page, fused_kv=fused))
+
+
+@pytest.mark.parametrize("kv", [4097, 30000])
+def test_decode_long(cuda_device, kv):
+    # every SM works on the same sequence: the joining of partial results
+    checked(Batch(32, 8, 128, [1], [kv], seed=kv, q_std=2.0))
+
+
+def test_decode_ragged_batch(cuda_device):
+    lens = [1 + (37 * i * i) % 3001 for i in range(70)]
+    checked(Batch(8, 2, 64, [1] * 70, lens, 32, True, seed=1))
+
+
+def test_empty_rows_and_sequences(cuda_device):
+    # no keys at all; no new tokens; fewer keys than new tokens (the first rows see nothing)
+    checked(Batch(4, 2, 128, [1, 0, 3, 1, 40, 0], [0, 5, 2, 70, 17, 0], spare_rows=3))
+    checked(Batch(4, 2, 128, [200, 1], [100, 0]))
+
+
+CHUNKS = [
+    ([2], [2]), ([4], [1000]), ([5, 1, 16, 3], [5, 300, 129, 64]), ([64], [64]), ([33, 130, 1], [64, 300, 17]),
+    ([257], [1000]), ([300, 129, 128], [300, 640, 128]), ([1000, 1, 7], [1000, 513, 2000]),
+]
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", CHUNKS)
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (2, 2, 64), (7, 1, 128), (20, 4, 64), (32, 1, 64)])
+def test_chunks(cuda_device, q_lens, kv_lens, hq, hk, d):
+    checked(Batch(hq, hk, d, q_lens, kv_lens, seed=len(q_lens), spare_rows=2))
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 1], [1, 100, 777]), ([9, 300], [400, 700]), ([1000], [1000])])
+@pytest.mark.parametrize("kw", [dict(window=1), dict(window=16), dict(window=200), dict(softcap=5.0),
+                                dict(window=100, softcap=30.0), dict(causal=False),
+                                dict(causal=False, window=50), dict(scale=0.5), dict(scale=-0.1)])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (7, 1, 64)])
+def test_options(cuda_device, q_lens, kv_lens, kw, hq, hk, d):
+    checked(Batch(hq, hk, d, q_lens, kv_lens, 16, seed=3, q_std=2.0), **kw)
+
+
+def test_large_scores(cuda_device):
+    # probabilities of nearly one key each, and maxima that keep rising along the keys
+    b = Batch(8, 2, 128, [1, 60], [900, 900], seed=4, q_std=8.0)
+    ramp = torch.linspace(0, 4, 900, device="cuda")[:, None, None].to(torch.bfloat16)
+    for k, (pg, off) in zip(b.keys, b.slots):
+        k.mul_(ramp)
+        b.k_cache[pg, off] = k
+    checked(b)
+
+
+def test_pages_shared_by_sequences(cuda_device):
+    # a common prefix: the second sequence's first pages are the first one's
+    b = Batch(4, 2, 128, [1, 20], [100, 120], 16, seed=5)
+    b.block_table[1, :5] = b.block_table[0, :5]
+    pg, off = b.slots[1]
+    pg[:80], b.keys[1][:80], b.values[1][:80] = b.slots[0][0][:80], b.keys[0][:80], b.values[0][:80]
+    checked(b)
+
+
+def test_nothing_past_the_window_is_needed(cuda_device):
+    # pages before the window are gone from the table
+    b = Batch(4, 2, 128, [1, 30], [600, 500], 16, seed=6)
+    b.block_table[0, :(600 - 64) // 16] = -1
+    b.block_table[1, :(500 - 30 + 1 - 64) // 16] = 1 << 29
+    checked(b, window=64)
+
+
+@pytest.mark.parametrize("q_len", [1, 100])
+def test_bad_page_reads_zeros_and_is_reported(cuda_device, q_len):
+    b = Batch(4, 2, 64, [q_len], [300], 32, seed=7)
+    b.block_table[0, 3] = b.k_cache.shape[0]
+    fd.device_status()
+    out, lse = run(b)
+    assert fd.device_status() == fd.FD_DEVICE_STATUS_BAD_PAGE
+    b.keys[0][96:128] = 0
+    b.values[0][96:128] = 0
+    check_attention(b, out, lse)
+
+
+def test_length_above_the_table_counts_as_its_end(cuda_device):
+    b = Batch(4, 2, 64, [1], [64], 16, seed=8)
+    b.kv_len += 1000
+    out, lse = run(b)
+    check_attention(b, out, lse)
+
+
+def test_strided_views(cuda_device):
+    b = Batch(4, 2, 128, [1, 40], [77, 90], 16, seed=9)
+    n = b.q.shape[0]
+    row = torch.zeros((n, 4 * 128 + 256), dtype=torch.bfloat16, device="cuda")
+    row[:, :512] = b.q.view(n, 512)
+    q = row[:, :512].view(n, 4, 128)
+    out = torch.zeros((4, n, 128), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    scratch = fd.paged_attention_scratch(2, n, 4, 2, 128, 40)
+    table = torch.full((2, 20), -1, dtype=torch.int32, device="cuda")
+    table[:, :b.block_table.shape[1]] = b.block_table
+    fd.paged_attention(q, b.k_cache, b.v_cache, b.q_start, b.kv_len, table[:, :b.block_table.shape[1]], 40,
+                       scratch, out=out)
+    check_attention(b, out)
+
+
+def test_offsets_past_32_bits(cuda_device):
+    # the last pages of a cache of more than 2^31 elements
+    hk, d, page = 8, 128, 64
+    pages = 2**31 // (hk * d * page) + 5
+    small = Batch(8, hk, d, [1, 30], [150, 100], page, seed=10)
+    kc = torch.empty((pages, page, hk, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    n = small.k_cache.shape[0]
+    kc[-n:], vc[-n:] = small.k_cache, small.v_cache
+    used = small.block_table < n
+    small.block_table[used] += pages - n
+    small.k_cache, small.v_cache = kc, vc
+    out, lse = run(small)
+    check_attention(small, out, lse)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [700, 90]), ([200, 3], [700, 90])])
+def test_graph_replayed_with_new_lengths(cuda_device, q_lens, kv_lens):
+    b = Batch(8, 2, 128, q_lens, kv_lens, 16, seed=11)
+    scratch = fd.paged_attention_scratch(2, b.q.shape[0], 8, 2, 128, b.max_q)
+    out, lse = run(b, scratch)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fd.paged_attention(b.q, *b.args(), b.max_q, scratch, out=out, lse=lse)
+    for cut in (0, 5, 80):
+        b.kv_len.copy_(torch.tensor([t - cut for t in kv_lens], dtype=torch.int32))
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        c = Batch.__new__(Batch)
+        c.__dict__ = dict(b.__dict__, kv_lens=[t - cut for t in kv_lens],
+                          keys=[k[:t - cut] for k, t in zip(b.keys, kv_lens)],
+                          values=[v[:t - cut] for v, t in zip(b.values, kv_lens)])
+        check_attention(c, out, lse)
+
+
+def test_two_streams_with_a_scratch_each(cuda_device):
+    b = Batch(32, 8, 128, [1], [3000], seed=12)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    scratch = [fd.paged_attention_scratch(1, 1, 32, 8, 128, 1) for _ in range(2)]
+    outs = [torch.zeros_like(b.q) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, sc, o in zip(streams, scratch, outs):
+            fd.paged_attention(b.q, *b.args(), 1, sc, out=o, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        check_attention(b, o)
+
+
+def test_back_to_back_with_programmatic_launch(cuda_device):
+    # calls that share a scratch, each started before the last has ended
+    b = Batch(32, 8, 128, [1, 1], [3000, 40], seed=13)
+    scratch = fd.paged_attention_scratch(2, 2, 32, 8, 128, 1)
+    prev = fd.set_pdl(True)
+    try:
+        outs = [run(b, scratch)[0] for _ in range(10)]
+    finally:
+        fd.set_pdl(prev)
+    check_attention(b, outs[0])
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
