@@ -531,7 +531,7 @@ int fd_device_status(fd_stream_t stream, unsigned *status, int clear) {
     // one word per file that records failures; pinned so the copies are truly asynchronous
     cudaError_t (*const readers[])(cudaStream_t, unsigned *, bool) = {
         status_gemv_tma, status_gemv_tc, status_nvfp4, status_decode_step, status_rope,
-        status_attn_rows};
+        status_attn_rows, status_attn_tc};
     constexpr int kWords = sizeof(readers) / sizeof(readers[0]);
     static thread_local unsigned *words = nullptr;
     if (!words) {

@@ -68,7 +68,7 @@ struct AttnArgs {
     float scale;      // multiplies q.k
     float softcap;    // 0: none
     unsigned *counters;  // one per CTA, zero between calls
-    float *partials;
+    float *partials;     // one slot for the first and one for the last item of each CTA
 };
 
 constexpr int kAttnMaxCtas = 256;             // largest grid (counters in the scratch)
@@ -84,6 +84,26 @@ __host__ __device__ constexpr int rows_slot_words(int d) { return kRowsM * (d + 
 cudaError_t launch_attn_rows(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                              cudaStream_t stream);
 cudaError_t status_attn_rows(cudaStream_t stream, unsigned *out, bool clear);
+
+// ---- attention of chunks (fd_attn_tc.cu)
+constexpr int kAttnTcTile = 128;    // keys of a tile
+constexpr int kAttnTcListed = 152;  // pairs of halves whose tiles can form one list
+// fp32 words of a partial result: 256 rows of head_dim, then (maximum, sum) of each
+__host__ __device__ constexpr int tc_slot_words(int d) { return 2 * 128 * (d + 2); }
+// Whether the tiles of all items are dealt out evenly (joined through the scratch) instead of one
+// item a CTA.
+inline bool attn_tc_listed(long long pairs, int batch, int kv_heads, int sms) {
+    return pairs <= kAttnTcListed && batch <= kAttnTcListed && pairs * kv_heads < 4 * sms;
+}
+cudaError_t launch_attn_tc(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
+                           cudaStream_t stream);
+cudaError_t status_attn_tc(cudaStream_t stream, unsigned *out, bool clear);
+
+// Which of the two: up to 16 rows a key head are one pass of the first; a group of more than 128
+// query heads does not fit the second's tile.
+inline bool attn_uses_tc(int max_q, int group) {
+    return (long long)max_q * group > kRowsM && group <= kAttnTcTile;
+}
 
 // ---- rotary positions (fd_rope.cu)
 struct RopeArgs {

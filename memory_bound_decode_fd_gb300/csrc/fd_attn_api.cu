@@ -304,7 +304,9 @@ size_t fd_paged_attention_scratch_bytes(int batch, int total_q, int q_heads, int
         q_heads <= 0 || kv_heads <= 0 || q_heads > FD_MAX_HEADS || q_heads % kv_heads != 0 ||
         (head_dim != 64 && head_dim != 128))
         return 0;
-    return kAttnCounterBytes + (size_t)2 * kAttnMaxCtas * rows_slot_words(head_dim) * sizeof(float);
+    const size_t slots = 2 * kAttnMaxCtas * sizeof(float);
+    return kAttnCounterBytes + slots * (attn_uses_tc(max_q, q_heads / kv_heads) ? tc_slot_words(head_dim)
+                                                                               : rows_slot_words(head_dim));
 }
 
 int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_paged_batch *batch,
@@ -350,11 +352,14 @@ int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_
     a.scale = scale, a.softcap = softcap;
     a.counters = static_cast<unsigned *>(scratch);
     a.partials = reinterpret_cast<float *>(static_cast<unsigned char *>(scratch) + kAttnCounterBytes);
-    const int box = cache->page_size < kRowsTile ? cache->page_size : kRowsTile;
+    const bool tc = attn_uses_tc(a.m.max_q, a.group);
+    const int tile = tc ? kAttnTcTile : kRowsTile;
+    const int box = cache->page_size < tile ? cache->page_size : tile;
     CUtensorMap mk, mv;
     if (!encode_cache(&mk, cache->k, dk, d, box, &a.ok) || !encode_cache(&mv, cache->v, dv, d, box, &a.ov))
         return api_status(cudaErrorInvalidValue);
-    return api_status(launch_attn_rows(a, mk, mv, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
+    return api_status(tc ? launch_attn_tc(a, mk, mv, st_) : launch_attn_rows(a, mk, mv, st_));
 }
 
 }  // extern "C"

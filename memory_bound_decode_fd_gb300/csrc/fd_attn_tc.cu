@@ -1,0 +1,741 @@
+// fd_attn_tc.cu - attention of chunks of new tokens over a paged cache on the fifth-generation
+// tensor cores.
+//
+// The rows of a key head are (new token, query head of its group) pairs, token by token; a CTA
+// takes 2 x 128 of them (two halves of floor(128 / group) tokens), so that each tile of keys and
+// values, copied once, serves all the heads that share it. Per tile of 128 keys and half:
+//     S = Q K^T (128 x 128 in tensor memory),  P = exp(S - m),  O = O + P V (in tensor memory).
+// Bound by the tensor cores: 4 * 128 * 128 * D flops a tile and half; the exponentials come next
+// (128 x 128 of them, half the tensor time at D = 128, all of it at D = 64).
+//
+//   * One warp copies key and value tiles (tensor-map copies of a page's 64-element columns) into a
+//     ring, one warp issues the MMAs, and two groups of four warps do the softmax of one half each,
+//     one row a thread. While one half is in the softmax the tensor cores run the other's P V and
+//     next S: per tile the MMA warp issues, for each half in turn, P V of this tile and then S of
+//     the next, and never waits for its own results.
+//   * S, P and O stay in tensor memory: P (bf16, two a column) takes the first half of S's
+//     columns and is the A operand of the second product from there. MMAs run in the order of
+//     issue, so the next S may overwrite P without a wait. Q and both operands of S are
+//     128-byte-swizzled K-major tiles; V is read as it lies, N-major.
+//   * The running maximum that P is taken against is only raised when a row's maximum has grown by
+//     more than 2^8 (then O is rescaled in tensor memory); up to there the sums hold the larger
+//     values exactly as well, fp32 and bf16 being floating point. P is rounded to bf16 (2^-8
+//     relative at most), the row's sum is that of the unrounded values, in fp32.
+//   * Work: enough items (pairs of halves times key heads) and each CTA takes one, the longest
+//     first. Few, and the tiles of all items form one list of which every CTA takes an equal run;
+//     an item that several CTAs share is joined by the last of them (a ticket), in CTA order.
+//   * Values of the first and last tile that no row of the item sees are cleared in shared memory
+//     before their MMA (0 x NaN): pages hold anything past the last token.
+//   * Every wait is bounded; a CTA that gives up writes NaN, drains its copies and MMAs and frees
+//     its tensor memory.
+#include <atomic>
+
+#include "fd_attn.h"
+#include "fd_tc.cuh"
+
+namespace fd {
+namespace {
+
+constexpr int kTile = 128;           // keys of a tile, rows of a half
+constexpr int kSoftmax = 256;        // threads of the two softmax groups
+constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kThreads = 384;          // the third group: MMA warp, copy warp, two idle
+// Registers: a softmax thread holds a row of S. 384 threads launch with 168 each (64512 in all);
+// 2 x 128 x 208 + 128 x 88 = 64512.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kMaxListed = kAttnTcListed;  // q tiles of one list
+constexpr float kRaise = 8.f;        // log2 units
+
+template <int D>
+struct TcShape {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kQ = kTile * D * 2;       // bytes of one half's queries
+    static constexpr int kStage = kTile * D * 2;   // a tile of keys or of values
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kSmem = 1024 + 2 * kQ + kStages * kStage;
+    // tensor memory columns: S (and P in its first half) and O of both halves
+    static constexpr uint32_t kS0 = 0, kO0 = 2 * kTile;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Makes the 32 registers of a tensor-memory load depend on the wait that came before.
+__device__ __forceinline__ void pin32(uint32_t *r) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Bounded wait that ignores the abort flag (copies landing, MMAs completing).
+__device__ __forceinline__ void wait_hw(uint64_t *bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!mbar_try_parity(bar, parity) && clock64() - t0 < kWaitLimitCycles) {
+    }
+}
+
+// mbar_wait_bounded with the slow path in line: a call would bind this kernel's registers to the
+// calling convention, which a kernel that moves registers between its warps has none left for.
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    if (mbar_try_parity(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_parity(bar, parity)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            record_wait_timeout();
+            return false;
+        }
+    }
+    return true;
+}
+
+// Tiles of 128 keys [a, b) that new tokens i0 .. i1 see together (a >= b: none).
+struct TileRange {
+    int a, b;
+};
+__device__ __forceinline__ TileRange tiles_of(const SeqInfo &s, const AttnArgs &p, int i0, int i1) {
+    const int lo = key_lo(s, i0, p.window), hi = key_hi(s, i1, p.causal);
+    if (i1 < i0 || hi <= lo) return {0, 0};
+    return {lo / kTile, (hi + kTile - 1) / kTile};
+}
+
+// One run of tiles of one item (pair of halves, key head).
+struct Segment {
+    SeqInfo s;
+    int b, hk;
+    int i0;            // first new token of the pair
+    int ja, jb;        // tiles of the run
+    TileRange h[2];    // of it, what each half sees
+    int lo, hi;        // keys that some row of the pair sees
+    int first, last;   // CTAs that share the item
+    long long next;    // tile of the list behind the run
+};
+
+__device__ __forceinline__ void clip_halves(Segment &g, const AttnArgs &a, int tokens, int from, int to) {
+    g.lo = key_lo(g.s, g.i0, a.window);
+    g.hi = key_hi(g.s, min(g.s.rows, g.i0 + 2 * tokens) - 1, a.causal);
+    g.ja = 1 << 30, g.jb = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i0 = g.i0 + e * tokens;
+        TileRange r = tiles_of(g.s, a, i0, min(g.s.rows, i0 + tokens) - 1);
+        r.a = max(r.a, from), r.b = min(r.b, to);
+        if (r.b <= r.a) r = {0, 0};
+        g.h[e] = r;
+        if (r.b > r.a) g.ja = min(g.ja, r.a), g.jb = max(g.jb, r.b);
+    }
+    if (g.jb == 0) g.ja = 0;
+}
+
+// Tiles of the pair that begins at token i0 (at least one, so that every row is written).
+__device__ __forceinline__ TileRange pair_tiles(const SeqInfo &s, const AttnArgs &a, int i0, int tokens) {
+    TileRange r = tiles_of(s, a, i0, min(s.rows, i0 + 2 * tokens) - 1);
+    if (r.b <= r.a) r = {0, 1};
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const AttnArgs a, int tokens /* of a half */, int listed) {
+    using T = TcShape<D>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages], done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag, last_s;
+    __shared__ int pick_b, pick_t;
+    __shared__ unsigned scan_s[kThreads / 32];
+    __shared__ unsigned prefix[kMaxListed + 1];       // tiles of one key head before each pair
+    __shared__ unsigned char pair_b[kMaxListed], pair_t[kMaxListed];
+    unsigned char *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+    const uint32_t q_base = smem_u32(smem), ring = q_base + 2 * T::kQ;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+        for (int e = 0; e < 2; ++e) {
+            mbar_init(&q_full[e], 4);
+            mbar_init(&s_full[e], 1);
+            mbar_init(&p_full[e], 4);
+            mbar_init(&o_full[e], 1);
+        }
+        for (int i = 0; i < T::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&done, 1);
+        abort_flag = 0;
+        pick_b = -1;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_slot, 512);
+        tmem_relinquish();
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+
+    // Sum over the block of one value a thread; returns the sum of the threads before this one.
+    auto scan = [&](unsigned v, unsigned *total) {
+        unsigned inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        __syncthreads();
+        if (lane == 31) scan_s[warp] = inc;
+        __syncthreads();
+        unsigned before = inc - v;
+        *total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += scan_s[w];
+            *total += scan_s[w];
+        }
+        return before;
+    };
+
+    // ---------------------------------------------------------------- what this CTA does
+    const int per = (a.m.batch + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, a.m.batch), b1 = min(b0 + per, a.m.batch);
+    auto pairs_of = [&](int b) { return (unsigned)((load_seq(a.m, b).rows + 2 * tokens - 1) / (2 * tokens)); };
+    unsigned mine = 0, n_pairs;
+    for (int b = b0; b < b1; ++b) mine += pairs_of(b);
+    unsigned at = scan(mine, &n_pairs);
+    long long begin = 0, end = 0, total = 0;
+    int G = 1, hk_single = 0;
+    bool work = true;
+    if (listed) {
+        n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
+        // one list: key head by key head, pair by pair, tile by tile
+        for (int b = b0; b < b1; ++b) {
+            const unsigned n = pairs_of(b);
+            for (unsigned t = 0; t < n && at < kMaxListed; ++t, ++at) {
+                pair_b[at] = (unsigned char)b;
+                pair_t[at] = (unsigned char)t;
+            }
+        }
+        __syncthreads();
+        unsigned tiles = 0, all;
+        if (tid < (int)n_pairs) {
+            const TileRange r = pair_tiles(load_seq(a.m, pair_b[tid]), a, pair_t[tid] * 2 * tokens, tokens);
+            tiles = r.b - r.a;
+        }
+        const unsigned before = scan(tiles, &all);
+        if (tid <= (int)n_pairs) prefix[tid] = before;
+        total = (long long)all * a.kv_heads;
+        G = (int)min((long long)gridDim.x, total);
+        work = (int)blockIdx.x < G;
+        if (work) {
+            begin = total * blockIdx.x / G;
+            end = total * (blockIdx.x + 1) / G;
+        }
+    } else {
+        // one item: the last pairs of a sequence see the most keys, so they come first
+        hk_single = blockIdx.x % a.kv_heads;
+        const int back = blockIdx.x / a.kv_heads;
+        work = back < (int)n_pairs;
+        const unsigned want = n_pairs - 1 - back;
+        if (work && at <= want && want < at + mine) {
+            unsigned left = want - at;
+            int b = b0;
+            for (unsigned n; left >= (n = pairs_of(b)); ++b) left -= n;
+            pick_b = b;
+            pick_t = (int)left;
+        }
+        end = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    if (!work) end = begin;
+
+    auto segment = [&](long long x) {
+        Segment g;
+        if (!listed) {
+            g.b = pick_b, g.hk = hk_single;
+            g.s = load_seq(a.m, g.b);
+            g.i0 = pick_t * 2 * tokens;
+            clip_halves(g, a, tokens, 0, 1 << 30);
+            g.first = g.last = 0;
+            g.next = 1;
+            return g;
+        }
+        const long long head = total / a.kv_heads;
+        g.hk = (int)(x / head);
+        const unsigned in_head = (unsigned)(x - g.hk * head);
+        int p = 0;
+        for (int up = (int)n_pairs - 1; p < up;) {  // the last pair with prefix[p] <= in_head
+            const int mid = (p + up + 1) >> 1;
+            if (prefix[mid] <= in_head)
+                p = mid;
+            else
+                up = mid - 1;
+        }
+        g.b = pair_b[p];
+        g.s = load_seq(a.m, g.b);
+        g.i0 = pair_t[p] * 2 * tokens;
+        const long long item0 = g.hk * head + prefix[p], item1 = g.hk * head + prefix[p + 1];
+        const TileRange r = pair_tiles(g.s, a, g.i0, tokens);
+        const long long stop = min(item1, end);
+        clip_halves(g, a, tokens, r.a + (int)(x - item0), r.a + (int)(stop - item0));
+        g.first = (int)(((item0 + 1) * G - 1) / total);
+        g.last = (int)((item1 * G - 1) / total);
+        g.next = stop;
+        return g;
+    };
+
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+        // ------------------------------------------------------------------ copies
+        const int box = min(1 << a.m.page_shift, kTile);
+        const int boxes = kTile / box;
+        const int ops = boxes * T::kHalves;  // at most 16
+        const int my_box = lane / T::kHalves, my_half = lane - my_box * T::kHalves;
+        const uint32_t dst0 = my_half * (kTile * 128) + my_box * box * 128;
+        const uint64_t policy = policy_evict_last();  // the other pairs of the sequence read them too
+        int stage = 0;
+        uint32_t phase = 0, issued = 0;
+        bool ok = true;
+        for (long long x = begin; x < end && ok;) {
+            const Segment g = segment(x);
+            x = g.next;
+            auto page_of = [&](int j) {
+                const int tok = j * kTile + my_box * box;
+                int page = a.m.num_pages;  // reads as zeros
+                if (j < g.jb && lane < ops && tok < g.hi && tok + box > g.lo) {
+                    const int id = a.m.table[(long long)g.b * a.m.table_stride + (tok >> a.m.page_shift)];
+                    if (id >= 0 && id < a.m.num_pages)
+                        page = id;
+                    else
+                        atomicOr(&g_wait_status, (unsigned)FD_DEVICE_STATUS_BAD_PAGE);
+                }
+                return page;
+            };
+            int next_page = page_of(g.ja);
+            for (int j = g.ja; j < g.jb && ok; ++j) {
+                const int page = next_page;
+                next_page = page_of(j + 1);
+                const int off = (j * kTile + my_box * box) & ((1 << a.m.page_shift) - 1);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_bounded(&empty[stage], phase ^ 1u, &abort_flag));
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[stage], T::kStage);
+                    __syncwarp();
+                    if (lane < ops) {
+                        const MapOrder ord = v ? a.ov : a.ok;
+                        const int y1 = ord.tok == 1 ? off : ord.head == 1 ? g.hk : page;
+                        const int y2 = ord.tok == 2 ? off : ord.head == 2 ? g.hk : page;
+                        const int y3 = ord.tok == 3 ? off : ord.head == 3 ? g.hk : page;
+                        tma_load_4d(smem + 2 * T::kQ + stage * T::kStage + dst0, v ? &map_v : &map_k, my_half * 64,
+                                    y1, y2, y3, &full[stage], policy);
+                    }
+                    ++issued;
+                    if (++stage == T::kStages) stage = 0, phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before the CTA ends
+            const uint32_t n = issued < (uint32_t)T::kStages ? issued : (uint32_t)T::kStages;
+            for (uint32_t i = issued - n; i < issued; ++i)
+                wait_hw(&full[i % T::kStages], (i / T::kStages) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // -------------------------------------------------------------------- MMAs
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D) | (1u << 16);  // B is N-major
+        int stage = 0;
+        uint32_t phase = 0, q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, &abort_flag));
+            return ok;
+        };
+        auto scores = [&](int e, int st) {  // S_e = Q_e K^T
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (uint32_t)(k >> 2) * (kTile * 128) + (k & 3) * 32;
+                    tc_mma_f16(tmem + T::kS0 + e * kTile, smem_desc_sw128(q_base + e * T::kQ + off),
+                               smem_desc_sw128(ring + st * T::kStage + off), idesc_s, k > 0);
+                }
+                tc_commit(&s_full[e]);
+            }
+            __syncwarp();
+        };
+        for (long long x = begin; x < end && ok;) {
+            const Segment g = segment(x);
+            x = g.next;
+            if (g.jb <= g.ja) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (g.h[e].b > g.h[e].a) {
+                    if (!wait(&q_full[e], q_ph[e])) break;
+                    q_ph[e] ^= 1u;
+                }
+            if (!ok || !wait(&full[stage], phase)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (g.ja >= g.h[e].a && g.ja < g.h[e].b) scores(e, stage);
+            if (lane == 0) tc_commit(&empty[stage]);
+            __syncwarp();
+            if (++stage == T::kStages) stage = 0, phase ^= 1u;
+            for (int j = g.ja; j < g.jb && ok; ++j) {
+                const int vs = stage;
+                const uint32_t vp = phase;
+                if (++stage == T::kStages) stage = 0, phase ^= 1u;
+                const int ks = stage;
+                const uint32_t kp = phase;
+                const bool more = j + 1 < g.jb;
+                if (!wait(&full[vs], vp)) break;
+                const int t0 = j * kTile;
+                if (t0 < g.lo || t0 + kTile > g.hi) {
+                    // rows of the tile that no row sees
+                    const int n0 = max(g.lo - t0, 0), n1 = min(g.hi - t0, kTile);
+                    for (int i = lane; i < kTile * T::kHalves * 8; i += 32) {
+                        const int row = (i >> 3) & (kTile - 1);
+                        if (row < n0 || row >= n1)
+                            sts_v4(ring + vs * T::kStage + i * 16, make_uint4(0, 0, 0, 0));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (j >= g.h[e].a && j < g.h[e].b) {
+                        if (!wait(&p_full[e], p_ph[e])) break;
+                        p_ph[e] ^= 1u;
+                        tc_fence_after();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int k = 0; k < kTile / 16; ++k)
+                                tc_mma_f16_ts(tmem + T::kO0 + e * kTile, tmem + T::kS0 + e * kTile + k * 8,
+                                              smem_desc_sw128_mn(ring + vs * T::kStage + k * 2048, kTile * 128, 1024),
+                                              idesc_o, (j > g.h[e].a) | (k > 0));
+                            if (j + 1 == g.h[e].b) tc_commit(&o_full[e]);
+                        }
+                        __syncwarp();
+                    }
+                    if (e == 1 && lane == 0) tc_commit(&empty[vs]);
+                    __syncwarp();
+                    if (more) {
+                        if (e == 0) {
+                            if (!wait(&full[ks], kp)) break;
+                            tc_fence_after();
+                        }
+                        if (j + 1 >= g.h[e].a && j + 1 < g.h[e].b) scores(e, ks);
+                        if (e == 1 && lane == 0) tc_commit(&empty[ks]);
+                        __syncwarp();
+                    }
+                }
+                if (more && ++stage == T::kStages) stage = 0, phase ^= 1u;
+            }
+        }
+        if (lane == 0) {  // nothing may be in flight when the memory is given back
+            tc_commit(&done);
+            wait_hw(&done, 0);
+        }
+        __syncwarp();
+    }
+    } else {
+        // ----------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int e = warp >> 2;                     // half
+        const int r = (warp & 3) * 32 + lane;        // row of the half, TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_addr = lane_base + T::kS0 + e * kTile, o_addr = lane_base + T::kO0 + e * kTile;
+        // A negative scale is put into Q's signs and a scale of 0 into zeros, so that what follows
+        // is monotone in S: the maximum of a row is taken before scale and cap.
+        const uint32_t q_and = a.scale == 0.f ? 0u : 0xFFFFFFFFu, q_xor = a.scale < 0.f ? 0x80008000u : 0u;
+        const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
+        const bool capped = a.softcap > 0.f;
+        const float mul = capped ? scale / a.softcap * (2.f * kLog2e) : scale * kLog2e;
+        const float cap_out = a.softcap * kLog2e;
+        // a score in log2 units; c tanh(y) = c (1 - 2 / (e^(2 y) + 1))
+        auto log2_score = [&](float v) {
+            return capped ? cap_out - __fdividef(2.f * cap_out, ex2(v * mul) + 1.f) : v * mul;
+        };
+        uint32_t s_ph = 0, o_ph = 0;
+        bool dead = false;
+        constexpr int kSlot = tc_slot_words(D);
+        for (long long x = begin; x < end;) {
+            const Segment g = segment(x);
+            x = g.next;
+            const int tl = r / a.group;
+            const int i = g.i0 + e * tokens + tl;
+            const int h = g.hk * a.group + r - tl * a.group;
+            const bool live = tl < tokens && i < g.s.rows;
+            const TileRange jr = e ? g.h[1] : g.h[0];
+            const bool any = jr.b > jr.a;
+            const int hi = live ? key_hi(g.s, i, a.causal) : 0, lo = live ? key_lo(g.s, i, a.window) : 0;
+            const int i_first = g.i0 + e * tokens, i_last = min(g.s.rows, i_first + tokens) - 1;
+            const int in_hi = key_hi(g.s, i_first, a.causal), in_lo = key_lo(g.s, i_last, a.window);
+            if (any) {
+                // this row of Q into the swizzled tile (rows without a token: zeros)
+                const uint16_t *q = a.q.p + (long long)(g.s.q0 + i) * a.q.ts + h * a.q.hs;
+                const uint32_t dst = q_base + e * T::kQ + r * 128;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 v = live ? *reinterpret_cast<const uint4 *>(q + c * 8) : make_uint4(0, 0, 0, 0);
+                    v.x = and_xor(v.x, q_and, q_xor), v.y = and_xor(v.y, q_and, q_xor);
+                    v.z = and_xor(v.z, q_and, q_xor), v.w = and_xor(v.w, q_and, q_xor);
+                    sts_v4(dst + (c >> 3) * (kTile * 128) + (((c & 7) ^ (r & 7)) << 4), v);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[e]);
+            }
+            float m = -INFINITY;  // what the exponentials are taken against, log2 units
+            float2 l2 = make_float2(0.f, 0.f);
+            for (int j = jr.a; j < jr.b; ++j) {
+                if (!dead) dead = !__all_sync(0xFFFFFFFFu, wait_bounded(&s_full[e], s_ph, &abort_flag));
+                if (dead) break;
+                s_ph ^= 1u;
+                tc_fence_after();
+                uint32_t su[kTile];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_x32(s_addr + 32 * c, su + 32 * c);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) pin32(su + 32 * c);
+                // columns [c0, c1) are visible; all of them inside the range that every row sees
+                const int t0 = j * kTile, c0 = lo - t0, c1 = hi - t0;
+                const bool masked = t0 < in_lo || t0 + kTile > in_hi;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c)
+                        mx[c & 3] = fmaxf(mx[c & 3], c >= c0 && c < c1 ? __uint_as_float(su[c]) : -INFINITY);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(su[c + 2 * k])), __uint_as_float(su[c + 2 * k + 1]));
+                }
+                const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const float top = raw == -INFINITY ? raw : log2_score(raw);
+                // raise the maximum: at the first keys, and when the row has grown by 2^kRaise
+                if (__any_sync(0xFFFFFFFFu, top > m && (m == -INFINITY || top - m > kRaise))) {
+                    const float up = fmaxf(top, m);
+                    const float f = m == -INFINITY ? 0.f : ex2(m - up);
+                    m = up;
+                    l2.x *= f, l2.y *= f;
+                    if (j > jr.a) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld_x32(o_addr + c, o);
+                            tmem_ld_wait();
+                            pin32(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st_x32(o_addr + c, o);
+                        }
+                    }
+                }
+                const float off = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t p[16];
+                    float *s = reinterpret_cast<float *>(su) + c;
+                    if (capped) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[k] = log2_score(s[k]) + off;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 y = ffma2(make_float2(s[k], s[k + 1]), make_float2(mul, mul), make_float2(off, off));
+                            s[k] = y.x, s[k + 1] = y.y;
+                        }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (c + k < c0 || c + k >= c1) s[k] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 v = make_float2(ex2(s[2 * k]), ex2(s[2 * k + 1]));
+                        l2 = fadd2(l2, v);
+                        p[k] = pack_bf16x2(v.x, v.y);
+                    }
+                    tmem_st_x16(s_addr + c / 2, p);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[e]);
+            }
+            // ------------------------------------------------------- the run's result
+            if (any) {
+                if (!dead) dead = !__all_sync(0xFFFFFFFFu, wait_bounded(&o_full[e], o_ph, &abort_flag));
+                o_ph ^= 1u;
+                tc_fence_after();
+            }
+            float l = l2.x + l2.y, m2 = m;
+            if (dead) l = NAN, m2 = 0.f;
+            const bool whole = g.first == g.last;
+            const long long tok = g.s.q0 + i;
+            if (whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                uint16_t *out = a.out.p + tok * a.out.ts + h * a.out.hs;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    if (any && !dead) {
+                        tmem_ld_x32(o_addr + c, o);
+                        tmem_ld_wait();
+                        pin32(o);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const float y0 = __uint_as_float(o[k + 2 * n]) * inv;
+                            const float y1 = __uint_as_float(o[k + 2 * n + 1]) * inv;
+                            w[n] = dead ? 0x7FC07FC0u : l == 0.f ? 0u : pack_bf16x2(y0, y1);
+                        }
+                        if (live) *reinterpret_cast<uint4 *>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                if (live && a.lse) a.lse[tok * a.q_heads + h] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
+            } else {
+                // slot: [D / 4][256 rows] of 4 floats, then (maximum, sum) of each row
+                float *slots = a.partials;
+                const int c = blockIdx.x;
+                float *slot = slots + (size_t)(2 * c + (c == g.first ? 1 : 0)) * kSlot;
+                const int row = e * kTile + r;
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32];
+                    if (any && !dead) {
+                        tmem_ld_x32(o_addr + d, o);
+                        tmem_ld_wait();
+                        pin32(o);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 v = any && !dead
+                            ? make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                                          __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (live) __stcg(reinterpret_cast<float4 *>(slot) + (d + k) / 4 * (2 * kTile) + row, v);
+                    }
+                }
+                if (live)
+                    __stcg(reinterpret_cast<float2 *>(slot + 2 * kTile * D) + row, make_float2(m2, l));
+                __threadfence();
+                named_bar_sync(1, kSoftmax);
+                if (tid == 0) {
+                    const unsigned ticket = atomicAdd(&a.counters[g.first], 1u);
+                    last_s = ticket == (unsigned)(g.last - g.first);
+                    if (last_s) a.counters[g.first] = 0;
+                    __threadfence();
+                }
+                named_bar_sync(1, kSoftmax);
+                if (last_s) {
+                    // rows (token, head) of the pair that exist, all (row, 4 elements) over the threads
+                    const int n_rows0 = min(tokens, g.s.rows - g.i0) * a.group;
+                    const int n_rows1 = max(0, min(tokens, g.s.rows - g.i0 - tokens)) * a.group;
+                    const int n_rows = n_rows0 + n_rows1;
+                    for (int idx = tid; idx < n_rows * (D / 4); idx += kSoftmax) {
+                        const int d4 = idx / n_rows;
+                        int rr = idx - d4 * n_rows;
+                        const int he = rr >= n_rows0;
+                        if (he) rr -= n_rows0;
+                        const int at_row = he * kTile + rr;
+                        float M = -INFINITY, L = 0.f;
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                        for (int k = g.first; k <= g.last; ++k) {
+                            const float *sl = slots + (size_t)(2 * k + (k == g.first ? 1 : 0)) * kSlot;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kTile * D) + at_row);
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(sl) + d4 * (2 * kTile) + at_row);
+                            const float up = fmaxf(M, ml.x), base = up == -INFINITY ? 0.f : up;
+                            const float f0 = ex2(M - base), f1 = ex2(ml.x - base);
+                            M = up;
+                            L = L * f0 + ml.y * f1;
+                            acc.x = acc.x * f0 + v.x * f1, acc.y = acc.y * f0 + v.y * f1;
+                            acc.z = acc.z * f0 + v.z * f1, acc.w = acc.w * f0 + v.w * f1;
+                        }
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+                        const int tt = rr / a.group;
+                        const int hh = g.hk * a.group + rr - tt * a.group;
+                        const long long to = g.s.q0 + g.i0 + he * tokens + tt;
+                        const bool bad = !(L == L);
+                        uint2 w = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                        if (bad) w = make_uint2(0x7FC07FC0u, 0x7FC07FC0u);
+                        *reinterpret_cast<uint2 *>(a.out.p + to * a.out.ts + hh * a.out.hs + 4 * d4) = w;
+                        if (d4 == 0 && a.lse)
+                            a.lse[to * a.q_heads + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+                    }
+                }
+                named_bar_sync(1, kSoftmax);
+            }
+            tc_fence_before();  // the loads of O, before the next run's MMAs
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    DeviceInfo di;
+    cudaError_t err = device_info(&di);
+    if (err != cudaSuccess) return err;
+    int dev = 0;
+    err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) & bit)) {
+        err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   TcShape<D>::kSmem);
+        if (err != cudaSuccess) return err;
+        if (dev < 64) attr_done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    // most pairs of halves that the batch can have (its lengths are device memory)
+    const int tokens = kTile / a.group;
+    const long long by_rows = a.m.total_q / (2 * tokens) + (long long)a.m.batch;
+    const long long by_seq = (long long)a.m.batch * ((a.m.max_q + 2 * tokens - 1) / (2 * tokens));
+    const long long pairs = by_rows < by_seq ? by_rows : by_seq;
+    const int sms = di.sm_count < kAttnMaxCtas ? di.sm_count : kAttnMaxCtas;
+    const bool listed = attn_tc_listed(pairs, a.m.batch, a.kv_heads, sms);
+    long long grid = pairs * a.kv_heads;
+    if (listed) {
+        const long long most = grid * ((a.m.capacity + kTile - 1) / kTile > 0 ? (a.m.capacity + kTile - 1) / kTile : 1);
+        grid = most < sms ? most : sms;
+    }
+    err = launch_kernel(attn_tc_kernel<D>, dim3((unsigned)grid), dim3(kThreads), (size_t)TcShape<D>::kSmem, stream,
+                        1, mk, mv, a, tokens, (int)listed);
+    if (err != cudaSuccess) return err;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
+                           cudaStream_t stream) {
+    return a.head_dim == 128 ? launch_d<128>(a, mk, mv, stream) : launch_d<64>(a, mk, mv, stream);
+}
+
+FD_DEFINE_STATUS_ACCESSOR(status_attn_tc)
+
+}  // namespace fd
