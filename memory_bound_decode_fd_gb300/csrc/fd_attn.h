@@ -62,7 +62,7 @@ struct AttnArgs {
     PagedMeta m;
     HeadsView q, out;
     float *lse;       // [total_q, q_heads] or null
-    MapOrder ok, ov;
+    MapOrder ok, ov;  // of the cache's tensor maps
     int q_heads, kv_heads, group, head_dim;
     int causal, window;
     float scale;      // multiplies q.k
@@ -78,7 +78,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // ---- attention of few rows per key head (fd_attn_rows.cu)
 constexpr int kRowsM = 16;      // query rows of one pass over the keys
-constexpr int kRowsTile = 64;   // keys of one pipeline stage
+constexpr int kRowsBox = 32;    // tokens of a copy (16 where a page has no more)
+__host__ __device__ constexpr int rows_warps(int d) { return d == 128 ? 4 : 8; }
 // fp32 words of a partial result: 16 rows of head_dim, then (maximum, sum) of each
 __host__ __device__ constexpr int rows_slot_words(int d) { return kRowsM * (d + 2); }
 cudaError_t launch_attn_rows(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,

@@ -353,8 +353,8 @@ int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_
     a.counters = static_cast<unsigned *>(scratch);
     a.partials = reinterpret_cast<float *>(static_cast<unsigned char *>(scratch) + kAttnCounterBytes);
     const bool tc = attn_uses_tc(a.m.max_q, a.group);
-    const int tile = tc ? kAttnTcTile : kRowsTile;
-    const int box = cache->page_size < tile ? cache->page_size : tile;
+    const int most = tc ? kAttnTcTile : kRowsBox;
+    const int box = cache->page_size < most ? cache->page_size : most;
     CUtensorMap mk, mv;
     if (!encode_cache(&mk, cache->k, dk, d, box, &a.ok) || !encode_cache(&mv, cache->v, dv, d, box, &a.ov))
         return api_status(cudaErrorInvalidValue);

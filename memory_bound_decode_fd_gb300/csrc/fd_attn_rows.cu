@@ -6,25 +6,27 @@
 // 16 multiply-adds per byte of the cache, far below what the tensor cores do, so what matters is
 // that every SM streams pages all the time.
 //
-//   * The keys of all (sequence, block of 16 rows, key head) items, in tiles of 64, form one long
-//     list, and CTA c of G takes tiles [T c / G, T (c + 1) / G) of it: every SM gets the same
-//     number of tiles whatever the lengths of the sequences, with nothing planned on the host (the
-//     lengths are device memory, a captured graph sees new ones). An item that several CTAs share
-//     is joined by the CTA that finishes last: each writes its rows' (maximum, sum, accumulator)
-//     to its own slot, takes a ticket, and the holder of the last ticket adds the slots in the
-//     order of the CTAs, so results do not depend on who is last.
-//   * One producer warp copies tiles (tensor-map copies of one page's 64-element columns each, all
-//     lanes issuing, page numbers read one tile ahead) into a ring of shared memory; four consumer
-//     warps take 16 keys of each tile. Each keeps its own running maximum, sum and fp32
-//     accumulator in registers (online softmax, one pass over the data) and they meet only at
-//     the end of an item, in shared memory.
+//   * The keys of all (sequence, block of 16 rows, key head) items, in tiles of 16 keys a warp,
+//     form one long list, and CTA c of G takes tiles [T c / G, T (c + 1) / G) of it: every SM gets
+//     the same number of tiles whatever the lengths of the sequences, with nothing planned on the
+//     host (the lengths are device memory, a captured graph sees new ones). An item that several
+//     CTAs share is joined by the CTA that finishes last: each writes its rows' (maximum, sum,
+//     accumulator) to its own slot, takes a ticket, and the holder of the last ticket adds the
+//     slots in the order of the CTAs, so results do not depend on who is last. Where whole items
+//     are dealt out evenly enough, no item is shared (kJoinTiles).
+//   * Each of the warps that compute has a warp that copies for it: its 32 keys and values of a
+//     tile, by tensor-map copies (64 elements of the tokens of a page, 128-byte swizzle) into a
+//     ring of their own in shared memory, across the ends of items; page numbers are read kAhead
+//     tiles early. Four copying warps, because one thread issues such a copy in about 60 ns: one
+//     warp for all kept 16-token pages (2 KB a copy) at 4.9 TB/s where 64-token pages ran at
+//     6.7. Plain 16-byte asynchronous copies stayed at 5.9 TB/s for every page size.
+//   * Each warp keeps its own running maximum, sum and fp32 accumulator in registers (online
+//     softmax, one pass over the data) and the warps meet only at the end of an item.
 //   * Scores are Q K^T with the rows as the M = 16 of mma.sync m16n8k16, so that the
 //     probabilities come out in the layout that P V takes as its A operand; rounded to bf16 there
 //     (V is bf16, both operands have one type), each by 2^-8 relative at most, while the sum is
-//     that of the unrounded ones. These legacy instructions are used on purpose: 128 of them a
-//     tile hide under its copy, and tcgen05 would pad the rows to 128.
-//   * Values outside the visible range are cleared in the operand registers: 0 x NaN would reach
-//     the sum otherwise, and pages hold anything past the last token.
+//     that of the unrounded ones. These legacy instructions are used on purpose: they hide under
+//     the copies, and tcgen05 would pad the rows to 128.
 #include <atomic>
 
 #include "fd_attn.h"
@@ -33,19 +35,27 @@
 namespace fd {
 namespace {
 
-constexpr int kWarps = 4;                       // consumers
-constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;
+// What joining the parts of an item costs, in tiles: a partial result written, a ticket, the
+// other parts read.
+constexpr int kJoinTiles = 6;
+
+constexpr int kKeys = 32;  // of a tile, a warp's
 
 template <int D>
 struct RowsShape {
-    static constexpr int kHalves = D / 64;             // 128-byte columns of a row
-    static constexpr int kTensor = kRowsTile * D * 2;  // bytes of a tile's keys (or values)
-    static constexpr int kStage = 2 * kTensor;
-    static constexpr int kStages = D == 128 ? 5 : 10;  // 160 KB in flight
-    static constexpr int kPitch = D + 8;               // floats; conflict-free accumulator rows
+    static constexpr int kWarps = rows_warps(D);
+    static constexpr int kConsumers = kWarps * 32;
+    static constexpr int kThreads = 2 * kConsumers;      // each computing warp, its copying warp
+    static constexpr int kTile = kWarps * kKeys;         // keys of a tile
+    static constexpr int kHalves = D / 64;               // 128-byte columns of a row
+    static constexpr int kColumn = kKeys * 128;          // bytes of one of a warp's keys
+    static constexpr int kPart = kHalves * kColumn;      // a warp's keys (or values) of a tile
+    static constexpr int kStages = 2;                    // 128 KB of shared memory in all
+    static constexpr int kRing = kStages * 2 * kPart;    // of one warp
+    static constexpr int kPitch = D + 8;                 // floats; conflict-free accumulator rows
     static constexpr int kMergeBytes = kWarps * kRowsM * kPitch * 4;
     static constexpr int kMlBytes = kWarps * kRowsM * 8;
+    static_assert(kMergeBytes >= kAttnMaxCtas * kRowsM * 8, "the parts' maxima and sums fit the buffer");
 };
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -73,6 +83,22 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// 4 bytes to shared memory, asynchronously.
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// A tile that a copying warp is to copy: its warp's first key, key head (-1: none is left), and
+// the pages of the first and second 16 keys (bit i of `read`: the page is needed).
+struct TileCopy {
+    int tok, hk, read, page[2];
+};
+constexpr int kAhead = 3;
+
 // One run of tiles of one item.
 struct Segment {
     SeqInfo s;
@@ -82,48 +108,72 @@ struct Segment {
     int rows;           // rows of the block
     int tile0;          // number of the first tile of the item's keys
     int from, to;       // the segment's tiles, counted in the item
-    int nt;             // tiles of the item
+    int nt;             // tiles of the item; 0: nothing to do
     long long item0;    // the item's first tile in the list
+    long long next;     // what comes after the segment
 };
 
 // Tiles that the keys of sequence s take (at least one, so that every row is written), and the
 // first of them. The same for all of the sequence's items.
+template <int TILE>
 __device__ __forceinline__ int seq_tiles(const SeqInfo &s, const AttnArgs &a, int *first) {
     *first = 0;
     if (s.rows <= 0) return 0;
     const int lo = key_lo(s, 0, a.window), hi = key_hi(s, s.rows - 1, a.causal);
     if (hi <= lo) return 1;
-    *first = lo / kRowsTile;
-    return (hi + kRowsTile - 1) / kRowsTile - *first;
+    *first = lo / TILE;
+    return (hi + TILE - 1) / TILE - *first;
 }
 
-// The segment that begins at tile x of the list and ends at `end` or with its item; `b` is a
-// sequence at or before x's.
-__device__ __forceinline__ Segment segment_at(const AttnArgs &a, const unsigned *prefix, int items,
-                                              long long x, long long end, int b) {
+// How the list of tiles is dealt out.
+struct Deal {
+    const unsigned *prefix;   // tiles of one item of each sequence before b
+    int items;                // of a sequence
+    long long total;          // tiles
+    int G;                    // CTAs that work
+    bool whole;               // items c, c + G, ... instead of tiles [begin, end)
+    long long begin, end;     // tiles, or items
+};
+
+// The segment at x (a tile of the list, or an item); `b` is a sequence at or before x's.
+template <int TILE>
+__device__ __forceinline__ Segment segment_at(const AttnArgs &a, const Deal &d, long long x, int b) {
     Segment g;
-    // the first b with prefix[b + 1] * items > x: this sequence, the next, or by bisection
-    if ((long long)prefix[b + 1] * items <= x && (long long)prefix[++b + 1] * items <= x) {
-        int up = a.m.batch - 1;
-        for (++b; b < up;) {
-            const int mid = (b + up) >> 1;
-            if ((long long)prefix[mid + 1] * items > x)
-                up = mid;
-            else
-                b = mid + 1;
+    const unsigned *prefix = d.prefix;
+    const int items = d.items;
+    if (d.whole) {
+        b = (int)((unsigned)x / (unsigned)items);
+        g.item = (int)x - b * items;
+        g.nt = (int)(prefix[b + 1] - prefix[b]);
+        g.from = 0, g.to = g.nt;
+        g.item0 = 0;
+        g.next = x + d.G;
+    } else {
+        // the first b with prefix[b + 1] * items > x: this sequence, the next, or by bisection
+        if ((long long)prefix[b + 1] * items <= x && (long long)prefix[++b + 1] * items <= x) {
+            int up = a.m.batch - 1;
+            for (++b; b < up;) {
+                const int mid = (b + up) >> 1;
+                if ((long long)prefix[mid + 1] * items > x)
+                    up = mid;
+                else
+                    b = mid + 1;
+            }
         }
+        g.nt = (int)(prefix[b + 1] - prefix[b]);
+        const long long in_seq = x - (long long)prefix[b] * items;
+        // 32 bits where they do: a 64-bit division is a hundred instructions
+        g.item = in_seq >> 32 ? (int)(in_seq / g.nt) : (int)((unsigned)in_seq / (unsigned)g.nt);
+        g.from = (int)(in_seq - (long long)g.item * g.nt);
+        g.item0 = x - g.from;
+        g.to = (int)min((long long)g.nt, d.end - g.item0);
+        g.next = g.item0 + g.to;
     }
     g.b = b;
     g.s = load_seq(a.m, b);
-    g.nt = (int)(prefix[b + 1] - prefix[b]);
-    const long long in_seq = x - (long long)prefix[b] * items;
-    g.item = (int)(in_seq / g.nt);
-    g.from = (int)(in_seq - (long long)g.item * g.nt);
-    g.item0 = x - g.from;
-    g.to = (int)min((long long)g.nt, end - g.item0);
     g.rb = g.item / a.kv_heads;
     g.hk = g.item - g.rb * a.kv_heads;
-    seq_tiles(g.s, a, &g.tile0);
+    seq_tiles<TILE>(g.s, a, &g.tile0);
     const int all = g.s.rows * a.group;
     g.rows = min(kRowsM, all - g.rb * kRowsM);  // <= 0: no such block in this sequence
     g.i0 = g.rb * kRowsM / a.group;
@@ -132,135 +182,188 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs &a, const unsigned 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(RowsShape<D>::kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const AttnArgs a, int row_blocks) {
     using S = RowsShape<D>;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kTile = S::kTile;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages];
-    __shared__ int abort_flag;
-    __shared__ int last_s;
-    __shared__ unsigned warp_sum[kThreads / 32];
     unsigned char *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-    float *merge = reinterpret_cast<float *>(smem + S::kStages * S::kStage);
-    float2 *ml = reinterpret_cast<float2 *>(smem + S::kStages * S::kStage + S::kMergeBytes);
-    unsigned *prefix = reinterpret_cast<unsigned *>(smem + S::kStages * S::kStage + S::kMergeBytes + S::kMlBytes);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
+    __shared__ int last_s, abort_flag;
+    __shared__ __align__(8) uint64_t full[kWarps][S::kStages], empty[kWarps][S::kStages];
+    __shared__ TileCopy next_tiles[kWarps][kAhead];
+    __shared__ unsigned warp_sum[2 * kWarps], warp_max[2 * kWarps];
+    float *merge = reinterpret_cast<float *>(smem + kWarps * S::kRing);
+    float2 *ml = reinterpret_cast<float2 *>(smem + kWarps * S::kRing + S::kMergeBytes);
+    unsigned *prefix = reinterpret_cast<unsigned *>(smem + kWarps * S::kRing + S::kMergeBytes + S::kMlBytes);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = tid / 32 % kWarps;  // of its kind
     if (tid == 0) {
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kWarps);
-        }
+        for (int w = 0; w < kWarps; ++w)
+            for (int i = 0; i < S::kStages; ++i) {
+                mbar_init(&full[w][i], 1);
+                mbar_init(&empty[w][i], 1);
+            }
         abort_flag = 0;
         fence_mbar_init();
     }
     grid_dep_wait();
     grid_dep_launch();
 
-    // The list: prefix[b] = tiles of one item of each sequence before b.
+    // ------------------------------------------------------------------- the list
+    Deal deal;
     {
         const int per = (a.m.batch + kThreads - 1) / kThreads;
         const int b0 = min(tid * per, a.m.batch), b1 = min(b0 + per, a.m.batch);
-        unsigned sum = 0;
+        unsigned sum = 0, most = 0;
         int first;
-        for (int b = b0; b < b1; ++b) sum += (unsigned)seq_tiles(load_seq(a.m, b), a, &first);
+        for (int b = b0; b < b1; ++b) {
+            const unsigned n = (unsigned)seq_tiles<kTile>(load_seq(a.m, b), a, &first);
+            prefix[b] = sum;  // of this thread's sequences
+            sum += n;
+            most = max(most, n);
+        }
         unsigned inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
             if (lane >= o) inc += up;
         }
-        if (lane == 31) warp_sum[warp] = inc;
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        if (lane == 31) warp_sum[tid >> 5] = inc, warp_max[tid >> 5] = most;
         __syncthreads();
-        unsigned at = inc - sum;
-        for (int w = 0; w < warp; ++w) at += warp_sum[w];
-        for (int b = b0; b < b1; ++b) {
-            prefix[b] = at;
-            at += (unsigned)seq_tiles(load_seq(a.m, b), a, &first);
+        unsigned before = inc - sum, all = 0;
+#pragma unroll
+        for (int w = 0; w < 2 * kWarps; ++w) {
+            if (w < (tid >> 5)) before += warp_sum[w];
+            all += warp_sum[w];
+            most = max(most, warp_max[w]);
         }
-        if (tid == kThreads - 1) prefix[a.m.batch] = at;
+        for (int b = b0; b < b1; ++b) prefix[b] += before;
+        if (tid == 0) prefix[a.m.batch] = all;
+        __syncthreads();
+        deal.prefix = prefix;
+        deal.items = row_blocks * a.kv_heads;
+        deal.total = (long long)all * deal.items;
+        const long long n = (long long)a.m.batch * deal.items;
+        const int c = blockIdx.x;
+        // whole items one after the other, or equal runs of tiles joined where they meet
+        const long long rounds = (n + gridDim.x - 1) / gridDim.x;
+        deal.whole = n < (1ll << 31) && rounds * most * gridDim.x <= deal.total + (long long)kJoinTiles * gridDim.x;
+        if (deal.whole) {
+            deal.G = gridDim.x;
+            deal.begin = c, deal.end = n;
+        } else {
+            // no more CTAs than tiles: each CTA between an item's first and last has a part of it
+            deal.G = (int)min((long long)gridDim.x, deal.total);
+            if (c >= deal.G) return;
+            deal.begin = deal.total * c / deal.G, deal.end = deal.total * (c + 1) / deal.G;
+        }
     }
-    __syncthreads();
-    const int items = row_blocks * a.kv_heads;
-    const long long total = (long long)prefix[a.m.batch] * items;
-    // no more CTAs than tiles: each of the CTAs between an item's first and last has a part of it
-    const int G = (int)min((long long)gridDim.x, total), c = blockIdx.x;
-    if (c >= G) return;
-    const long long begin = total * c / G, end = total * (c + 1) / G;
 
-    if (warp == kWarps) {
-        // ------------------------------------------------------------------ producer
-        const int box = min(1 << a.m.page_shift, kRowsTile);  // tokens of one copy
-        const int boxes = kRowsTile / box;
-        const int per_tensor = boxes * S::kHalves;
-        const int ops = 2 * per_tensor;  // at most 16
-        const bool is_v = lane >= per_tensor;
-        const int r = lane - (is_v ? per_tensor : 0);
-        const int my_box = r / S::kHalves, my_half = r - my_box * S::kHalves;
-        const uint32_t dst0 = (is_v ? S::kTensor : 0) + my_half * (kRowsTile * 128) + my_box * box * 128;
-        const CUtensorMap *map = is_v ? &map_v : &map_k;
-        const MapOrder ord = is_v ? a.ov : a.ok;
+    const uint32_t ring = smem_u32(smem) + warp * S::kRing;
+    if (tid >= S::kConsumers) {
+        // ---------------------------------------------------------------------- copies
         const uint64_t policy = policy_evict_first();
-        Segment g = segment_at(a, prefix, items, begin, end, 0);
-        int tile = g.from;
-        long long x = begin;
-        // this lane's page for the tile at hand; num_pages (reads as zeros) where none is needed
-        auto page_of = [&](const Segment &sg, int t) {
-            const int tok = (sg.tile0 + t) * kRowsTile + my_box * box;
-            const int lo = key_lo(sg.s, 0, a.window), hi = key_hi(sg.s, sg.s.rows - 1, a.causal);
-            int page = a.m.num_pages;
-            if (lane < ops && tok < hi && tok + box > lo) {
-                const int id = a.m.table[(long long)sg.b * a.m.table_stride + (tok >> a.m.page_shift)];
-                if (id >= 0 && id < a.m.num_pages)
-                    page = id;
-                else
-                    atomicOr(&g_wait_status, (unsigned)FD_DEVICE_STATUS_BAD_PAGE);
-            }
-            return page;
-        };
-        int page = page_of(g, tile);
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        long long issued = 0;
-        while (true) {
-            const int tok = (g.tile0 + tile) * kRowsTile + my_box * box;
-            const int off = tok & ((1 << a.m.page_shift) - 1);
-            const int hk = g.hk, this_page = page;
-            // read the next tile's page numbers before this one waits for room
-            ++x;
-            const bool more = x < end;
-            if (more) {
-                if (++tile == g.to) {
-                    g = segment_at(a, prefix, items, x, end, g.b);
-                    tile = g.from;
+        const int page_mask = (1 << a.m.page_shift) - 1;
+        // What is to be copied, kAhead tiles before its turn: by then its page number has arrived,
+        // copied to the description asynchronously (a load would hold this warp up in order).
+        volatile TileCopy *ahead = next_tiles[warp];
+        Segment g;
+        g.to = 0;
+        int tile = 0, lo = 0, hi = 0, b_at = 0;
+        long long x = deal.begin;
+        bool more = true;
+        auto describe = [&](int entry) {
+            while (more && ++tile >= g.to) {
+                if (x >= deal.end) {
+                    more = false;
+                    break;
                 }
-                page = page_of(g, tile);
+                g = segment_at<kTile>(a, deal, x, b_at);
+                b_at = g.b;
+                x = g.next;
+                tile = g.from - 1;
+                lo = key_lo(g.s, 0, a.window), hi = key_hi(g.s, g.s.rows - 1, a.causal);
             }
-            ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, &abort_flag);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&full[stage], S::kStage);
-            __syncwarp();
-            if (lane < ops) {
-                const int y1 = ord.tok == 1 ? off : ord.head == 1 ? hk : this_page;
-                const int y2 = ord.tok == 2 ? off : ord.head == 2 ? hk : this_page;
-                const int y3 = ord.tok == 3 ? off : ord.head == 3 ? hk : this_page;
-                tma_load_4d(smem + stage * S::kStage + dst0, map, my_half * 64, y1, y2, y3, &full[stage], policy);
+            if (lane == 0) {
+                volatile TileCopy &t = ahead[entry];
+                const int tok = (g.tile0 + tile) * kTile + warp * kKeys;
+                const int *row = a.m.table + (long long)g.b * a.m.table_stride;
+                int read = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int first = tok + 16 * i;
+                    if (more && first < hi && first + 16 > lo) {
+                        copy4(smem_u32(const_cast<int *>(&t.page[i])), row + (first >> a.m.page_shift));
+                        read |= 1 << i;
+                    }
+                }
+                t.tok = tok, t.hk = more ? g.hk : -1, t.read = read;
             }
-            ++issued;
-            if (++stage == S::kStages) stage = 0, phase ^= 1u;
-            if (!more) break;
+        };
+#pragma unroll 1
+        for (int i = 0; i < kAhead; ++i) {
+            describe(i);
+            copy_commit();
         }
-        if (!ok && lane == 0) {
-            // a consumer gave up: wait (bounded) for the copies in flight before the CTA ends
-            const long long n = issued < S::kStages ? issued : S::kStages;
-            for (long long i = issued - n; i < issued; ++i) {
+        int entry = 0, slot = 0;
+        uint32_t phase = 1, issued = 0;
+        bool ok = true;
+        while (true) {
+            copy_wait<kAhead - 1>();  // the description's pages
+            __syncwarp();
+            const int hk = ahead[entry].hk, tok = ahead[entry].tok, read = ahead[entry].read;
+            int page[2] = {ahead[entry].page[0], ahead[entry].page[1]};
+            if (hk < 0) break;
+            __syncwarp();
+            describe(entry);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[warp][slot], phase, &abort_flag));
+            if (!ok) break;
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if ((read >> i & 1) && (unsigned)page[i] >= (unsigned)a.m.num_pages)
+                        atomicOr(&g_wait_status, (unsigned)FD_DEVICE_STATUS_BAD_PAGE);
+                    // a copy from behind the last page fills zeros
+                    if (!(read >> i & 1) || (unsigned)page[i] >= (unsigned)a.m.num_pages) page[i] = a.m.num_pages;
+                }
+                uint64_t *const bar = &full[warp][slot];
+                mbar_arrive_expect_tx(bar, 2 * S::kPart);
+                unsigned char *const dst = smem + warp * S::kRing + slot * 2 * S::kPart;
+                auto copy = [&](int first, int pg) {  // the box of tokens that begins with key `first`
+                    const int at = (tok + first) & page_mask;
+                    const int k1 = a.ok.tok == 1 ? at : a.ok.head == 1 ? hk : pg;
+                    const int k2 = a.ok.tok == 2 ? at : a.ok.head == 2 ? hk : pg;
+                    const int k3 = a.ok.tok == 3 ? at : a.ok.head == 3 ? hk : pg;
+                    const int v1 = a.ov.tok == 1 ? at : a.ov.head == 1 ? hk : pg;
+                    const int v2 = a.ov.tok == 2 ? at : a.ov.head == 2 ? hk : pg;
+                    const int v3 = a.ov.tok == 3 ? at : a.ov.head == 3 ? hk : pg;
+#pragma unroll
+                    for (int h = 0; h < S::kHalves; ++h) {
+                        unsigned char *const to = dst + h * S::kColumn + first * 128;
+                        tma_load_4d(to, &map_k, 64 * h, k1, k2, k3, bar, policy);
+                        tma_load_4d(to + S::kPart, &map_v, 64 * h, v1, v2, v3, bar, policy);
+                    }
+                };
+                // boxes of 16 tokens, or of 32 (one page, whichever half of it is needed)
+                copy(0, a.m.page_shift == 4 || (read & 1) ? page[0] : page[1]);
+                if (a.m.page_shift == 4) copy(16, page[1]);
+            }
+            __syncwarp();
+            ++issued;
+            copy_commit();
+            if (++slot == S::kStages) slot = 0, phase ^= 1u;
+            if (++entry == kAhead) entry = 0;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before the CTA ends
+            const uint32_t n = issued < (uint32_t)S::kStages ? issued : (uint32_t)S::kStages;
+            for (uint32_t i = issued - n; i < issued; ++i) {
                 const long long t0 = clock64();
-                while (!mbar_try_parity(&full[i % S::kStages], (uint32_t)((i / S::kStages) & 1)) &&
+                while (!mbar_try_parity(&full[warp][i % S::kStages], (i / S::kStages) & 1u) &&
                        clock64() - t0 < kWaitLimitCycles) {
                 }
             }
@@ -268,23 +371,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
-    // ---------------------------------------------------------------------- consumers
+    // ------------------------------------------------------------------------- the work
     const int g8 = lane >> 2, c2 = (lane & 3) * 2;  // accumulator row and column of this lane
     const float to_log2 = a.scale * kLog2e;
     const float cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
-    // ldmatrix rows: keys (lane & 7) + 8 * (lane >> 4) of the warp's 16, chunk bit (lane >> 3) & 1
-    const int k_row = warp * 16 + (lane & 7) + ((lane >> 4) << 3), k_bit = (lane >> 3) & 1;
+    // ldmatrix rows: keys (lane & 7) + 8 * (lane >> 4), chunk bit (lane >> 3) & 1
+    const int k_row = (lane & 7) + ((lane >> 4) << 3), k_bit = (lane >> 3) & 1;
     // values, transposed: keys (lane & 15), chunk bit lane >> 4
-    const int v_row = warp * 16 + (lane & 15), v_bit = lane >> 4;
-    const uint32_t ring = smem_u32(smem);
-    int stage = 0;
+    const int v_row = lane & 15, v_bit = lane >> 4;
+    int stage = 0, b_at = 0;
     uint32_t phase = 0;
     bool dead = false;
-    int b_at = 0;
-    for (long long x = begin; x < end;) {
-        const Segment g = segment_at(a, prefix, items, x, end, b_at);
+    for (long long x = deal.begin; x < deal.end;) {
+        const Segment g = segment_at<kTile>(a, deal, x, b_at);
         b_at = g.b;
-        x = g.item0 + g.to;
+        x = g.next;
+        if (g.nt == 0) continue;
         // the rows of this lane: tokens, heads and visible keys
         uint32_t qf[D / 16][4];
         int hi[2], lo[2];
@@ -310,71 +412,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
+#pragma unroll 1
         for (int t = g.from; t < g.to; ++t) {
-            if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, &abort_flag));
+            if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[warp][stage], phase, &abort_flag));
             if (dead) break;
-            const uint32_t kb = ring + stage * S::kStage, vb = kb + S::kTensor;
-            const int tok = (g.tile0 + t) * kRowsTile + warp * 16;  // the warp's first key
-            // a warp's 16 keys outside every row's range (the ends of a window) add nothing
-            if (g.rows > 0 && tok < any_hi && tok + 16 > any_lo) {
-                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const uint32_t kb = ring + stage * 2 * S::kPart, vb = kb + S::kPart;
+            uint64_t *const done = &empty[warp][stage];
+            if (++stage == S::kStages) stage = 0, phase ^= 1u;
+            const int tok = (g.tile0 + t) * kTile + warp * kKeys;  // the warp's first key
+            // a warp's keys outside every row's range (the ends of a window) add nothing
+            if (g.rows <= 0 || tok >= any_hi || tok + kKeys <= any_lo) {
+                if (lane == 0) mbar_arrive(done);
+                continue;
+            }
+            constexpr int kN = kKeys / 8;  // blocks of 8 keys
+            float s[kN][4];
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
+            for (int n = 0; n < kN; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+                for (int n = 0; n < kN; n += 2) {
                     uint32_t kf[4];
-                    const int chunk = (ks & 3) * 2 + k_bit;
-                    ldsm_x4(kf, kb + (ks >> 2) * (kRowsTile * 128) + k_row * 128 + ((chunk ^ (k_row & 7)) << 4));
-                    mma_bf16(s[0], qf[ks], kf[0], kf[1]);
-                    mma_bf16(s[1], qf[ks], kf[2], kf[3]);
+                    ldsm_x4(kf, kb + (ks >> 2) * S::kColumn + (n * 8 + k_row) * 128 +
+                                    ((((ks & 3) * 2 + k_bit) ^ (k_row & 7)) << 4));
+                    mma_bf16(s[n], qf[ks], kf[0], kf[1]);
+                    mma_bf16(s[n + 1], qf[ks], kf[2], kf[3]);
                 }
-                const bool inside = tok >= in_lo && tok + 16 <= in_hi;
-                float mx[2] = {-INFINITY, -INFINITY};
+            }
+            const bool inside = tok >= in_lo && tok + kKeys <= in_hi;
+            if (a.softcap > 0.f) {  // c tanh(y) = c (1 - 2 / (e^(2 y) + 1))
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[n][i] = cap_out * (1.f - __fdividef(2.f, ex2(s[n][i] * cap_in * (2.f * kLog2e)) + 1.f));
+            } else {
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[n][i] *= to_log2;
+            }
+            if (!inside) {
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float v = s[n][i];
-                        if (a.softcap > 0.f)  // c tanh(y) = c (1 - 2 / (e^(2 y) + 1))
-                            v = cap_out * (1.f - __fdividef(2.f, ex2(v * cap_in * (2.f * kLog2e)) + 1.f));
-                        else
-                            v *= to_log2;
                         const int key = tok + n * 8 + c2 + (i & 1);
-                        if (!inside && (key < lo[i >> 1] || key >= hi[i >> 1])) v = -INFINITY;
-                        s[n][i] = v;
-                        mx[i >> 1] = fmaxf(mx[i >> 1], v);
+                        if (key < lo[i >> 1] || key >= hi[i >> 1]) s[n][i] = -INFINITY;
                     }
-                float up[2];
+            }
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
-                    mx[e] = fmaxf(mx[e], m[e]);
-                    up[e] = mx[e] > m[e] ? ex2(m[e] - mx[e]) : 1.f;  // 0 from the first maximum on
-                    m[e] = mx[e];
-                }
-                if (__any_sync(0xFFFFFFFFu, up[0] != 1.f || up[1] != 1.f)) {
-                    l[0] *= up[0], l[1] *= up[1];
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        o[n][0] *= up[0], o[n][1] *= up[0];
-                        o[n][2] *= up[1], o[n][3] *= up[1];
-                    }
+                for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(mx[e], s[n][2 * e]), s[n][2 * e + 1]);
+            float up[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 1));
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], 2));
+                mx[e] = fmaxf(mx[e], m[e]);
+                up[e] = mx[e] > m[e] ? ex2(m[e] - mx[e]) : 1.f;  // 0 from the first maximum on
+                m[e] = mx[e];
+            }
+            if (__any_sync(0xFFFFFFFFu, up[0] != 1.f || up[1] != 1.f)) {
+                l[0] *= up[0], l[1] *= up[1];
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    o[n][0] *= up[0], o[n][1] *= up[0];
+                    o[n][2] *= up[1], o[n][3] *= up[1];
                 }
-                const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+            }
+            const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+            for (int h = 0; h < kKeys / 16; ++h) {
                 uint32_t p[4];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float p0 = ex2(s[n][0] - m0), p1 = ex2(s[n][1] - m0);
-                    const float p2 = ex2(s[n][2] - m1), p3 = ex2(s[n][3] - m1);
+                    const float p0 = ex2(s[2 * h + n][0] - m0), p1 = ex2(s[2 * h + n][1] - m0);
+                    const float p2 = ex2(s[2 * h + n][2] - m1), p3 = ex2(s[2 * h + n][3] - m1);
                     l[0] += p0 + p1, l[1] += p2 + p3;
                     p[2 * n] = pack_bf16x2(p0, p1);
                     p[2 * n + 1] = pack_bf16x2(p2, p3);
                 }
-                // values of this lane's operand registers: keys c2, c2 + 1 and c2 + 8, c2 + 9
+                // values that no row sees are cleared in the operand registers, which hold keys c2,
+                // c2 + 1 and c2 + 8, c2 + 9: 0 x NaN would reach the sum otherwise
                 uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
                 if (!inside) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int key = tok + 8 * e + c2;
+                        const int key = tok + 16 * h + 8 * e + c2;
                         keep[e] = (key >= any_lo && key < any_hi ? 0xFFFFu : 0u) |
                                   (key + 1 >= any_lo && key + 1 < any_hi ? 0xFFFF0000u : 0u);
                     }
@@ -382,15 +510,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
                     uint32_t vf[4];
-                    const int chunk = (n & 3) * 2 + v_bit;
-                    ldsm_x4_t(vf, vb + (n >> 2) * (kRowsTile * 128) + v_row * 128 + ((chunk ^ (v_row & 7)) << 4));
+                    ldsm_x4_t(vf, vb + (n >> 2) * S::kColumn + (16 * h + v_row) * 128 +
+                                      ((((n & 3) * 2 + v_bit) ^ (v_row & 7)) << 4));
                     mma_bf16(o[2 * n], p, vf[0] & keep[0], vf[1] & keep[1]);
                     mma_bf16(o[2 * n + 1], p, vf[2] & keep[0], vf[3] & keep[1]);
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
-            if (++stage == S::kStages) stage = 0, phase ^= 1u;
+            if (lane == 0) mbar_arrive(done);
         }
 
         // ------------------------------------------------ the warps of this segment meet
@@ -407,14 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float2 *>(mine + n * 8) = make_float2(o[n][0], o[n][1]);
             *reinterpret_cast<float2 *>(mine + 8 * S::kPitch + n * 8) = make_float2(o[n][2], o[n][3]);
         }
-        named_bar_sync(1, kConsumers);
+        named_bar_sync(1, S::kConsumers);
         // CTAs that share the item, in the order of their tiles
-        const int first = (int)(((g.item0 + 1) * G - 1) / total);
-        const int last = (int)(((g.item0 + g.nt) * G - 1) / total);
-        const bool whole = first == last;
-        float *slots = a.partials;
+        const bool whole = g.from == 0 && g.to == g.nt;
         constexpr int kSlot = rows_slot_words(D);
-        float *slot = slots + (size_t)(2 * c + (c == first ? 1 : 0)) * kSlot;
         const int n4 = max(g.rows, 0) * (D / 4);
         auto finish = [&](int row, int d4, float M, float L, float4 acc) {
             const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -424,7 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint2 *>(a.out.p + tok * a.out.ts + h * a.out.hs + 4 * d4) = w;
             if (d4 == 0 && a.lse) a.lse[tok * a.q_heads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
         };
-        for (int idx = tid; idx < n4; idx += kConsumers) {
+        int first = 0, last = 0;
+        float *slot_out = a.partials;
+        if (!whole) {
+            first = (int)(((g.item0 + 1) * deal.G - 1) / deal.total);
+            last = (int)(((g.item0 + g.nt) * deal.G - 1) / deal.total);
+            slot_out += (size_t)(2 * blockIdx.x + ((int)blockIdx.x == first ? 1 : 0)) * kSlot;
+        }
+        for (int idx = tid; idx < n4; idx += S::kConsumers) {
             const int row = idx / (D / 4), d4 = idx - row * (D / 4);
             float2 s[kWarps];
             float M = -INFINITY;
@@ -444,12 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (whole) {
                 finish(row, d4, M, L, acc);
             } else {
-                __stcg(reinterpret_cast<float4 *>(slot + row * D + 4 * d4), acc);
-                if (d4 == 0) __stcg(reinterpret_cast<float2 *>(slot + kRowsM * D + 2 * row), make_float2(M, L));
+                __stcg(reinterpret_cast<float4 *>(slot_out + row * D + 4 * d4), acc);
+                if (d4 == 0) __stcg(reinterpret_cast<float2 *>(slot_out + kRowsM * D + 2 * row), make_float2(M, L));
             }
         }
         if (!whole) __threadfence();
-        named_bar_sync(1, kConsumers);  // also: the buffers are free for the next segment
+        named_bar_sync(1, S::kConsumers);  // also: the buffers are free for the next segment
         if (whole) continue;
         if (tid == 0) {
             const unsigned ticket = atomicAdd(&a.counters[first], 1u);
@@ -457,28 +587,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (last_s) a.counters[first] = 0;
             __threadfence();
         }
-        named_bar_sync(1, kConsumers);
+        named_bar_sync(1, S::kConsumers);
         if (last_s) {
-            for (int idx = tid; idx < n4; idx += kConsumers) {
+            // all parts' maxima and sums at once, then every part's rows with their weights
+            float2 *parts = reinterpret_cast<float2 *>(merge);
+            const int n = last - first + 1;
+            for (int i = tid; i < n * kRowsM; i += S::kConsumers) {
+                const int k = first + (i >> 4);
+                if ((i & 15) < g.rows)
+                    parts[i] = __ldcg(reinterpret_cast<const float2 *>(
+                        a.partials + (size_t)(2 * k + (k == first ? 1 : 0)) * kSlot + kRowsM * D + 2 * (i & 15)));
+            }
+            named_bar_sync(1, S::kConsumers);
+            for (int idx = tid; idx < n4; idx += S::kConsumers) {
                 const int row = idx / (D / 4), d4 = idx - row * (D / 4);
                 float M = -INFINITY, L = 0.f;
+                for (int k = 0; k < n; ++k) M = fmaxf(M, parts[k * kRowsM + row].x);
+                const float base = M == -INFINITY ? 0.f : M;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int k = first; k <= last; ++k) {
-                    const float *sl = slots + (size_t)(2 * k + (k == first ? 1 : 0)) * kSlot;
-                    const float2 s = __ldcg(reinterpret_cast<const float2 *>(sl + kRowsM * D + 2 * row));
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(sl + row * D + 4 * d4));
-                    const float top = fmaxf(M, s.x), base = top == -INFINITY ? 0.f : top;
-                    const float f0 = ex2(M - base), f1 = ex2(s.x - base);
-                    M = top;
-                    L = L * f0 + s.y * f1;
-                    acc.x = acc.x * f0 + v.x * f1, acc.y = acc.y * f0 + v.y * f1;
-                    acc.z = acc.z * f0 + v.z * f1, acc.w = acc.w * f0 + v.w * f1;
+#pragma unroll 8
+                for (int k = 0; k < n; ++k) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                        a.partials + (size_t)(2 * (first + k) + (k == 0 ? 1 : 0)) * kSlot + row * D + 4 * d4));
+                    const float2 s = parts[k * kRowsM + row];
+                    const float f = ex2(s.x - base);
+                    L = fmaf(s.y, f, L);
+                    acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+                    acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
                 }
                 finish(row, d4, M, L, acc);
             }
         }
-        named_bar_sync(1, kConsumers);  // last_s is read before the next segment writes it
+        named_bar_sync(1, S::kConsumers);  // the buffers and last_s are read before the next segment writes them
     }
 }
 
@@ -492,7 +632,7 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     int dev = 0;
     err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
-    constexpr size_t kFixed = 1024 + S::kStages * S::kStage + S::kMergeBytes + S::kMlBytes;
+    constexpr size_t kFixed = 1024 + S::kWarps * S::kRing + S::kMergeBytes + S::kMlBytes;
     static_assert(kFixed + 4 * (FD_MAX_BATCH + 1) + 1024 <= 227 * 1024, "shared memory");
     const uint64_t bit = 1ull << (dev & 63);
     if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) & bit)) {
@@ -502,10 +642,11 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
         if (dev < 64) attr_done.fetch_or(bit, std::memory_order_acq_rel);
     }
     const long long row_blocks = ((long long)a.m.max_q * a.group + kRowsM - 1) / kRowsM;
-    const long long most = (long long)a.m.batch * row_blocks * a.kv_heads * ((a.m.capacity + kRowsTile - 1) / kRowsTile);
+    const long long tiles = (a.m.capacity + S::kTile - 1) / S::kTile;
+    const long long most = (long long)a.m.batch * row_blocks * a.kv_heads * (tiles > 0 ? tiles : 1);
     long long grid = di.sm_count < kAttnMaxCtas ? di.sm_count : kAttnMaxCtas;
     if (grid > most) grid = most;
-    err = launch_kernel(attn_rows_kernel<D>, dim3((unsigned)grid), dim3(kThreads),
+    err = launch_kernel(attn_rows_kernel<D>, dim3((unsigned)grid), dim3(S::kThreads),
                         kFixed + 4 * (size_t)(a.m.batch + 1), stream, 1, mk, mv, a, (int)row_blocks);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();

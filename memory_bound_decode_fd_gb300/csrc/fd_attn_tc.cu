@@ -45,6 +45,8 @@ constexpr int kThreads = 384;          // the third group: MMA warp, copy warp, 
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMaxListed = kAttnTcListed;  // q tiles of one list
 constexpr float kRaise = 8.f;        // log2 units
+// What joining the parts of an item costs, in tiles.
+constexpr int kJoinTiles = 6;
 
 template <int D>
 struct TcShape {
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, last_s;
     __shared__ int pick_b, pick_t;
-    __shared__ unsigned scan_s[kThreads / 32];
+    __shared__ unsigned scan_s[kThreads / 32], max_s[kThreads / 32];
     __shared__ unsigned prefix[kMaxListed + 1];       // tiles of one key head before each pair
     __shared__ unsigned char pair_b[kMaxListed], pair_t[kMaxListed];
     unsigned char *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned at = scan(mine, &n_pairs);
     long long begin = 0, end = 0, total = 0;
     int G = 1, hk_single = 0;
-    bool work = true;
+    bool work = true, whole_items = false;
     if (listed) {
         n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
         // one list: key head by key head, pair by pair, tile by tile
@@ -228,12 +230,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const unsigned before = scan(tiles, &all);
         if (tid <= (int)n_pairs) prefix[tid] = before;
+        unsigned most = __reduce_max_sync(0xFFFFFFFFu, tiles);
+        if (lane == 0) max_s[warp] = most;
+        __syncthreads();
+        for (int w = 0; w < kThreads / 32; ++w) most = max(most, max_s[w]);
         total = (long long)all * a.kv_heads;
-        G = (int)min((long long)gridDim.x, total);
-        work = (int)blockIdx.x < G;
-        if (work) {
-            begin = total * blockIdx.x / G;
-            end = total * (blockIdx.x + 1) / G;
+        // whole items, dealt out in turn, or equal runs of tiles joined where they meet
+        const int n = (int)n_pairs * a.kv_heads;
+        const long long rounds = (n + gridDim.x - 1) / gridDim.x;
+        whole_items = rounds * most * gridDim.x <= total + (long long)kJoinTiles * gridDim.x;
+        if (whole_items) {
+            G = gridDim.x;
+            begin = blockIdx.x, end = n;
+            work = begin < end;
+        } else {
+            G = (int)min((long long)gridDim.x, total);
+            work = (int)blockIdx.x < G;
+            if (work) {
+                begin = total * blockIdx.x / G;
+                end = total * (blockIdx.x + 1) / G;
+            }
         }
     } else {
         // one item: the last pairs of a sequence see the most keys, so they come first
@@ -265,6 +281,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             clip_halves(g, a, tokens, 0, 1 << 30);
             g.first = g.last = 0;
             g.next = 1;
+            return g;
+        }
+        if (whole_items) {  // the last pairs of a sequence see the most keys: they come first
+            const int p = (int)x / a.kv_heads, back = (int)n_pairs - 1 - p;
+            g.hk = (int)x - p * a.kv_heads;
+            g.b = pair_b[back];
+            g.s = load_seq(a.m, g.b);
+            g.i0 = pair_t[back] * 2 * tokens;
+            clip_halves(g, a, tokens, 0, 1 << 30);
+            g.first = g.last = 0;
+            g.next = x + G;
             return g;
         }
         const long long head = total / a.kv_heads;
@@ -502,26 +529,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (dead) break;
                 s_ph ^= 1u;
                 tc_fence_after();
-                uint32_t su[kTile];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_x32(s_addr + 32 * c, su + 32 * c);
-                tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) pin32(su + 32 * c);
+                // All of the row for its maximum. The second half is read again for the exponentials:
+                // kept, the row and what the rest needs would not fit the registers.
+                uint32_t s01[64];
                 // columns [c0, c1) are visible; all of them inside the range that every row sees
                 const int t0 = j * kTile, c0 = lo - t0, c1 = hi - t0;
                 const bool masked = t0 < in_lo || t0 + kTile > in_hi;
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (masked) {
+                {
+                    uint32_t s23[64];
+                    tmem_ld_x32(s_addr, s01);
+                    tmem_ld_x32(s_addr + 32, s01 + 32);
+                    tmem_ld_x32(s_addr + 64, s23);
+                    tmem_ld_x32(s_addr + 96, s23 + 32);
+                    tmem_ld_wait();
+                    pin32(s01), pin32(s01 + 32), pin32(s23), pin32(s23 + 32);
+                    if (masked) {
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c)
-                        mx[c & 3] = fmaxf(mx[c & 3], c >= c0 && c < c1 ? __uint_as_float(su[c]) : -INFINITY);
-                } else {
+                        for (int c = 0; c < 64; ++c) {
+                            mx[c & 3] = fmaxf(mx[c & 3], c >= c0 && c < c1 ? __uint_as_float(s01[c]) : -INFINITY);
+                            mx[c & 3] = fmaxf(mx[c & 3], c + 64 >= c0 && c + 64 < c1 ? __uint_as_float(s23[c]) : -INFINITY);
+                        }
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 8)
+                        for (int c = 0; c < 64; c += 4)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(su[c + 2 * k])), __uint_as_float(su[c + 2 * k + 1]));
+                            for (int k = 0; k < 4; ++k)
+                                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s01[c + k])), __uint_as_float(s23[c + k]));
+                    }
                 }
                 const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const float top = raw == -INFINITY ? raw : log2_score(raw);
@@ -545,10 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float off = m == -INFINITY ? 0.f : -m;
-#pragma unroll
-                for (int c = 0; c < kTile; c += 32) {
+                // 32 columns of S into 16 of P
+                auto exponentials = [&](uint32_t *su, int c) {
+                    float *s = reinterpret_cast<float *>(su);
                     uint32_t p[16];
-                    float *s = reinterpret_cast<float *>(su) + c;
                     if (capped) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) s[k] = log2_score(s[k]) + off;
@@ -571,7 +606,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         p[k] = pack_bf16x2(v.x, v.y);
                     }
                     tmem_st_x16(s_addr + c / 2, p);
-                }
+                };
+                uint32_t s23[64];
+                tmem_ld_x32(s_addr + 64, s23);
+                tmem_ld_x32(s_addr + 96, s23 + 32);
+                exponentials(s01, 0);
+                tmem_ld_wait();  // P's next columns are those of the scores just read
+                pin32(s23), pin32(s23 + 32);
+                exponentials(s01 + 32, 32);
+                exponentials(s23, 64);
+                exponentials(s23 + 32, 96);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -650,35 +694,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n_rows0 = min(tokens, g.s.rows - g.i0) * a.group;
                     const int n_rows1 = max(0, min(tokens, g.s.rows - g.i0 - tokens)) * a.group;
                     const int n_rows = n_rows0 + n_rows1;
-                    for (int idx = tid; idx < n_rows * (D / 4); idx += kSoftmax) {
-                        const int d4 = idx / n_rows;
-                        int rr = idx - d4 * n_rows;
+                    // 32 elements of a row at a time: 8 loads of each part in flight
+                    for (int idx = tid; idx < n_rows * (D / 32); idx += kSoftmax) {
+                        const int d0 = idx / n_rows * 8;
+                        int rr = idx % n_rows;
                         const int he = rr >= n_rows0;
                         if (he) rr -= n_rows0;
                         const int at_row = he * kTile + rr;
+                        const float *sl = slots + (size_t)(2 * g.first + 1) * kSlot;
                         float M = -INFINITY, L = 0.f;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
+                        for (int k = g.first; k <= g.last; ++k)
+                            M = fmaxf(M, __ldcg(slots + (size_t)(2 * k + (k == g.first ? 1 : 0)) * kSlot + 2 * kTile * D + 2 * at_row));
+                        const float base = M == -INFINITY ? 0.f : M;
+                        float4 acc[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
                         for (int k = g.first; k <= g.last; ++k) {
-                            const float *sl = slots + (size_t)(2 * k + (k == g.first ? 1 : 0)) * kSlot;
+                            if (k > g.first) sl = slots + (size_t)(2 * k) * kSlot;
                             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kTile * D) + at_row);
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(sl) + d4 * (2 * kTile) + at_row);
-                            const float up = fmaxf(M, ml.x), base = up == -INFINITY ? 0.f : up;
-                            const float f0 = ex2(M - base), f1 = ex2(ml.x - base);
-                            M = up;
-                            L = L * f0 + ml.y * f1;
-                            acc.x = acc.x * f0 + v.x * f1, acc.y = acc.y * f0 + v.y * f1;
-                            acc.z = acc.z * f0 + v.z * f1, acc.w = acc.w * f0 + v.w * f1;
+                            const float f = ex2(ml.x - base);
+                            L = fmaf(ml.y, f, L);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(sl) + (d0 + q) * (2 * kTile) + at_row);
+                                acc[q].x = fmaf(v.x, f, acc[q].x), acc[q].y = fmaf(v.y, f, acc[q].y);
+                                acc[q].z = fmaf(v.z, f, acc[q].z), acc[q].w = fmaf(v.w, f, acc[q].w);
+                            }
                         }
                         const float inv = L == 0.f ? 0.f : 1.f / L;
                         const int tt = rr / a.group;
                         const int hh = g.hk * a.group + rr - tt * a.group;
                         const long long to = g.s.q0 + g.i0 + he * tokens + tt;
-                        const bool bad = !(L == L);
-                        uint2 w = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                        if (bad) w = make_uint2(0x7FC07FC0u, 0x7FC07FC0u);
-                        *reinterpret_cast<uint2 *>(a.out.p + to * a.out.ts + hh * a.out.hs + 4 * d4) = w;
-                        if (d4 == 0 && a.lse)
+                        uint16_t *out = a.out.p + to * a.out.ts + hh * a.out.hs + 4 * d0;
+#pragma unroll
+                        for (int q = 0; q < 8; q += 2)
+                            *reinterpret_cast<uint4 *>(out + 4 * q) = make_uint4(
+                                pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv),
+                                pack_bf16x2(acc[q + 1].x * inv, acc[q + 1].y * inv),
+                                pack_bf16x2(acc[q + 1].z * inv, acc[q + 1].w * inv));
+                        if (d0 == 0 && a.lse)
                             a.lse[to * a.q_heads + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
                     }
                 }
