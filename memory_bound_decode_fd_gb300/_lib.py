@@ -103,6 +103,8 @@ _lib = None
 def load(path: Path | None = None) -> ctypes.CDLL:
     """Load libfd.so once and attach the signatures. Raises FdLibraryMissing if absent."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

@@ -3,87 +3,125 @@ key/value cache and the attention over it. Argument marshalling only, like kerne
 
 from __future__ import annotations
 
-import math
 import struct
 
 import torch
 
 from . import _lib
-from .kernels import _check_tensor, _device_of, _on_device, _ptr, _stream_handle
+from .kernels import _on_device, _stream_handle
+
+# These calls are a few microseconds on the GPU when decoding, so what the host does for them
+# counts: checks read each attribute once, structures are packed without ctypes objects, and what
+# exactly is wrong with an argument is looked into only when something is.
+
+_Tensor, _BF16, _I32 = torch.Tensor, torch.bfloat16, torch.int32
 
 # fd_heads, fd_paged_cache and fd_paged_batch of include/fd.h, packed as the C compiler lays them out
 _HEADS = struct.Struct("=Qqqi4x")
 _CACHE = struct.Struct("=QQqqqqqqiiii")
 _BATCH = struct.Struct("=QQQiiiii4x")
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-def _heads(name: str, t: torch.Tensor, tokens: int | None = None, heads: int | None = None,
-           head_dim: int | None = None) -> bytes:
-    """The fd_heads of a bf16 [tokens, heads, head_dim] tensor (any token and head strides)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+
+def _refuse(name: str, t, dtype: torch.dtype, shape, dims: str) -> Exception:
+    """What is wrong with tensor argument `name` (`shape`: its sizes, None where any will do)."""
+    if not isinstance(t, _Tensor):
+        return TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the fd kernels have no CPU path)")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
-    n, h, d = t.shape
-    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or \
-            (head_dim is not None and d != head_dim):
-        raise ValueError(f"{name} must have shape {(tokens or n, heads or h, head_dim or d)}, got {(n, h, d)}")
-    ts, hs, ds = t.stride()
-    if ds != 1 and d > 1:
-        raise ValueError(f"{name} must have unit stride along head_dim")
-    return _HEADS.pack(t.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0, h)
+        return ValueError(f"{name} must be a CUDA tensor (the fd kernels have no CPU path)")
+    if t.dtype != dtype:
+        return TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    got = tuple(t.shape)
+    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        return ValueError(f"{name} must be {dims} of shape [{want}], got {got}")
+    return ValueError(f"{name} must have unit stride along its last dimension and be on the device of the "
+                      f"call's other tensors, got strides {t.stride()} on {t.device}")
 
 
-def _cache(k: torch.Tensor, v: torch.Tensor) -> tuple[bytes, int, int, int]:
-    """(fd_paged_cache, kv_heads, head_dim, page_size) of bf16 [num_pages, page_size, kv_heads, head_dim] tensors."""
+def _device(t) -> int:
+    """The device index of a call's first tensor (-1: not a CUDA tensor, which its own check refuses)."""
+    return t.get_device() if isinstance(t, _Tensor) else -1
+
+
+def _heads(name: str, t: _Tensor, dev: int, n=None, h=None, d=None) -> bytes:
+    """The fd_heads of a bf16 [tokens, heads, head_dim] tensor (any token and head strides)."""
+    if isinstance(t, _Tensor) and t.dtype is _BF16 and t.get_device() == dev >= 0:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 3 and stride[2] == 1 and (n is None or shape[0] == n) and (h is None or shape[1] == h) \
+                and (d is None or shape[2] == d):
+            return _HEADS.pack(t.data_ptr(), stride[0] if shape[0] > 1 else 0,
+                               stride[1] if shape[1] > 1 else 0, shape[1])
+    raise _refuse(name, t, _BF16, (n, h, d), "[tokens, heads, head_dim]")
+
+
+def _new(like: _Tensor, shape) -> tuple[_Tensor, bytes]:
+    """A new contiguous bf16 [tokens, heads, head_dim] tensor beside `like`, and its fd_heads."""
+    t = torch.empty(shape, dtype=_BF16, device=like.device)
+    n, h, d = shape
+    return t, _HEADS.pack(t.data_ptr(), h * d, d, h)
+
+
+def _flat(name: str, t: _Tensor, dev: int, dtype: torch.dtype, n=None) -> int:
+    """The address of a contiguous one-dimensional tensor."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev >= 0:
+        shape = t.shape
+        if len(shape) == 1 and (n is None or shape[0] == n) and t.is_contiguous():
+            return t.data_ptr()
+    raise _refuse(name, t, dtype, (n,), "a contiguous vector")
+
+
+def _cache(k: _Tensor, v: _Tensor, dev: int) -> tuple[bytes, int, int]:
+    """(fd_paged_cache, kv_heads, head_dim) of bf16 [num_pages, page_size, kv_heads, head_dim] tensors."""
     for name, t in (("k_cache", k), ("v_cache", v)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (the fd kernels have no CPU path)")
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [num_pages, page_size, kv_heads, head_dim], got {tuple(t.shape)}")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name} must have unit stride along head_dim")
-    if k.shape != v.shape:
-        raise ValueError(f"k_cache and v_cache differ in shape: {tuple(k.shape)}, {tuple(v.shape)}")
-    pages, page, heads, d = k.shape
+        if not (isinstance(t, _Tensor) and t.dtype is _BF16 and t.get_device() == dev >= 0 and t.dim() == 4
+                and t.stride(3) == 1):
+            raise _refuse(name, t, _BF16, (None,) * 4, "[num_pages, page_size, kv_heads, head_dim]")
+    shape = k.shape
+    if shape != v.shape:
+        raise ValueError(f"k_cache and v_cache differ in shape: {tuple(shape)}, {tuple(v.shape)}")
+    pages, page, heads, d = shape
     a, b = k.stride(), v.stride()
     return (_CACHE.pack(k.data_ptr(), v.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2], pages, page, heads, d),
-            heads, d, page)
+            heads, d)
 
 
-def _batch(q_start, kv_len, block_table, total_q: int, max_q: int) -> bytes:
-    if not isinstance(kv_len, torch.Tensor) or kv_len.dim() != 1:
-        raise ValueError("kv_len must be an int32 [batch] tensor")
+def _batch(q_start, kv_len, block_table, dev: int, total_q: int, max_q: int) -> bytes:
+    kv = _flat("kv_len", kv_len, dev, _I32)
     batch = kv_len.shape[0]
-    _check_tensor("q_start", q_start, torch.int32, (batch + 1,))
-    _check_tensor("kv_len", kv_len, torch.int32)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError("block_table must be an int32 [batch, max_pages] tensor")
-    if not block_table.is_cuda:
-        raise ValueError("block_table must be a CUDA tensor (the fd kernels have no CPU path)")
-    if block_table.dtype != torch.int32:
-        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
-    pages = block_table.shape[1]
-    row, col = block_table.stride()
-    if pages > 1 and col != 1:
-        raise ValueError("block_table must have unit stride along a sequence's pages")
-    return _BATCH.pack(q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
-                       row if batch > 1 else pages, batch, total_q, max_q, pages)
+    start = _flat("q_start", q_start, dev, _I32, batch + 1)
+    if isinstance(block_table, _Tensor) and block_table.dtype is _I32 and block_table.get_device() == dev:
+        shape, stride = block_table.shape, block_table.stride()
+        if len(shape) == 2 and shape[0] == batch and (stride[1] == 1 or shape[1] <= 1):
+            return _BATCH.pack(start, kv, block_table.data_ptr(), stride[0] if batch > 1 else shape[1], batch,
+                               total_q, max_q, shape[1])
+    raise _refuse("block_table", block_table, _I32, (batch, None), "[batch, max_pages]")
 
 
-def _inv_freq(inv_freq: torch.Tensor, head_dim: int) -> int:
-    _check_tensor("inv_freq", inv_freq, torch.float64)
-    if inv_freq.dim() != 1 or not 1 <= inv_freq.shape[0] <= head_dim // 2:
-        raise ValueError(f"inv_freq must be [rot_dim / 2] with 2 <= rot_dim <= head_dim={head_dim}")
-    return 2 * inv_freq.shape[0]
+def _inv_freq(inv_freq: _Tensor, dev: int, head_dim: int) -> tuple[int, int]:
+    ptr = _flat("inv_freq", inv_freq, dev, torch.float64)
+    pairs = inv_freq.shape[0]
+    if not 1 <= pairs <= head_dim // 2:
+        raise ValueError(f"inv_freq must be [rot_dim / 2] with 2 <= rot_dim <= head_dim={head_dim}, got [{pairs}]")
+    return ptr, 2 * pairs
+
+
+def _stream(stream, dev: int) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream_handle(stream, torch.device("cuda", dev)).value
+
+
+def _call(dev: int, fn, *args):
+    """fn(*args) with `dev` as the current device."""
+    if dev == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with _on_device(torch.device("cuda", dev)):
+            st = fn(*args)
+    if st:
+        _lib.check(st)
 
 
 def rope(
@@ -105,29 +143,26 @@ def rope(
     (2i, 2i + 1) if interleaved, else (i, i + rot_dim / 2). q_out, k_out: allocated if None; q
     and k themselves for a rotation in place.
     """
-    qb = _heads("q", q)
-    n, h, d = q.shape
-    _check_tensor("positions", positions, torch.int32, (n,))
-    rot = _inv_freq(inv_freq, d)
-    if q_out is None:
-        q_out = torch.empty((n, h, d), dtype=torch.bfloat16, device=q.device)
-    qo = _heads("q_out", q_out, n, h, d)
+    dev = _device(q)
+    qb = _heads("q", q, dev)
+    shape = n, _, d = q.shape
+    pos = _flat("positions", positions, dev, _I32, n)
+    freq, rot = _inv_freq(inv_freq, dev, d)
     kb = ko = None
     if k is not None:
-        kb = _heads("k", k, n, None, d)
+        kb = _heads("k", k, dev, n, None, d)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
-        ko = _heads("k_out", k_out, n, k.shape[1], d)
-        dev = _device_of(q, k, q_out, k_out, positions, inv_freq)
+            k_out, ko = _new(k, k.shape)
+        else:
+            ko = _heads("k_out", k_out, dev, *k.shape)
     elif k_out is not None:
         raise ValueError("k_out without k")
+    if q_out is None:
+        q_out, qo = _new(q, shape)
     else:
-        dev = _device_of(q, q_out, positions, inv_freq)
-    lib = _lib.load()
-    with _on_device(dev):
-        st = lib.fd_rope(qb, kb, qo, ko, _ptr(positions), _ptr(inv_freq), n, d, rot,
-                         int(bool(interleaved)), scale, _stream_handle(stream, dev))
-    _lib.check(st)
+        qo = _heads("q_out", q_out, dev, *shape)
+    _call(dev, _lib.load().fd_rope, qb, kb, qo, ko, pos, freq, n, d, rot, 1 if interleaved else 0, scale,
+          _stream(stream, dev))
     return q_out, k_out
 
 
@@ -158,26 +193,21 @@ def rope_append(
     in its cache). q_out: allocated if None; may be q (in place). Rows past q_start[batch] are not
     written.
     """
-    cache, hk, d, _ = _cache(k_cache, v_cache)
-    qb = _heads("q", q, None, None, d)
-    n, h, _ = q.shape
-    kb = _heads("k", k, n, hk, d)
-    vb = _heads("v", v, n, hk, d)
-    rot = _inv_freq(inv_freq, d)
-    batch = _batch(q_start, kv_len, block_table, n, n)
-    if positions is not None:
-        _check_tensor("positions", positions, torch.int32, (n,))
+    dev = _device(q)
+    cache, hk, d = _cache(k_cache, v_cache, dev)
+    qb = _heads("q", q, dev, None, None, d)
+    shape = n, _, _ = q.shape
+    kb = _heads("k", k, dev, n, hk, d)
+    vb = _heads("v", v, dev, n, hk, d)
+    freq, rot = _inv_freq(inv_freq, dev, d)
+    batch = _batch(q_start, kv_len, block_table, dev, n, n)
+    pos = None if positions is None else _flat("positions", positions, dev, _I32, n)
     if q_out is None:
-        q_out = torch.empty((n, h, d), dtype=torch.bfloat16, device=q.device)
-    qo = _heads("q_out", q_out, n, h, d)
-    dev = _device_of(q, k, v, k_cache, v_cache, q_start, kv_len, block_table, inv_freq, q_out,
-                     *(() if positions is None else (positions,)))
-    lib = _lib.load()
-    with _on_device(dev):
-        st = lib.fd_rope_append(qb, kb, vb, qo, cache, batch,
-                                None if positions is None else _ptr(positions), _ptr(inv_freq), rot,
-                                int(bool(interleaved)), scale, _stream_handle(stream, dev))
-    _lib.check(st)
+        q_out, qo = _new(q, shape)
+    else:
+        qo = _heads("q_out", q_out, dev, *shape)
+    _call(dev, _lib.load().fd_rope_append, qb, kb, vb, qo, cache, batch, pos, freq, rot,
+          1 if interleaved else 0, scale, _stream(stream, dev))
     return q_out
 
 
@@ -221,28 +251,27 @@ def paged_attention(
     q_heads] output, the log of each row's sum of exponentials. A row that sees no key gives zeros
     and -inf.
     """
-    cache, hk, d, _ = _cache(k_cache, v_cache)
-    qb = _heads("q", q, None, None, d)
-    n, h, _ = q.shape
-    if h % hk:
+    dev = _device(q)
+    cache, hk, d = _cache(k_cache, v_cache, dev)
+    qb = _heads("q", q, dev, None, None, d)
+    shape = n, h, _ = q.shape
+    if hk == 0 or h % hk:
         raise ValueError(f"q has {h} heads: not a multiple of the cache's {hk}")
     if max_q < 0 or window < 0:
         raise ValueError("max_q and window must not be negative")
-    batch = _batch(q_start, kv_len, block_table, n, min(max_q, n))
-    _check_tensor("scratch", scratch, torch.uint8)
+    batch = _batch(q_start, kv_len, block_table, dev, n, min(max_q, n))
+    work = _flat("scratch", scratch, dev, torch.uint8)
     if out is None:
-        out = torch.empty((n, h, d), dtype=torch.bfloat16, device=q.device)
-    ob = _heads("out", out, n, h, d)
-    more = ()
+        out, ob = _new(q, shape)
+    else:
+        ob = _heads("out", out, dev, *shape)
+    lse_ptr = None
     if lse is not None:
-        _check_tensor("lse", lse, torch.float32, (n, h))
-        more = (lse,)
-    dev = _device_of(q, k_cache, v_cache, q_start, kv_len, block_table, scratch, out, *more)
-    lib = _lib.load()
-    with _on_device(dev):
-        st = lib.fd_paged_attention(qb, cache, batch, ob, None if lse is None else _ptr(lse),
-                                    1.0 / math.sqrt(d) if scale is None else scale, int(bool(causal)),
-                                    min(int(window), 2**31 - 1), softcap, _ptr(scratch), scratch.numel(),
-                                    _stream_handle(stream, dev))
-    _lib.check(st)
+        if not isinstance(lse, _Tensor) or lse.dtype != torch.float32 or lse.get_device() != dev \
+                or lse.shape != shape[:2] or not lse.is_contiguous():
+            raise _refuse("lse", lse, torch.float32, (n, h), "contiguous [total_q, q_heads]")
+        lse_ptr = lse.data_ptr()
+    _call(dev, _lib.load().fd_paged_attention, qb, cache, batch, ob, lse_ptr,
+          d**-0.5 if scale is None else scale, 1 if causal else 0, min(window, 2**31 - 1), softcap, work,
+          scratch.shape[0], _stream(stream, dev))
     return out
