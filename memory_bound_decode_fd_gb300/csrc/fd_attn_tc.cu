@@ -21,9 +21,10 @@
 //     more than 2^8 (then O is rescaled in tensor memory); up to there the sums hold the larger
 //     values exactly as well, fp32 and bf16 being floating point. P is rounded to bf16 (2^-8
 //     relative at most), the row's sum is that of the unrounded values, in fp32.
-//   * Work: enough items (pairs of halves times key heads) and each CTA takes one, the longest
-//     first. Few, and the tiles of all items form one list of which every CTA takes an equal run;
-//     an item that several CTAs share is joined by the last of them (a ticket), in CTA order.
+//   * Work: up to kMaxListed pairs of halves and the grid is one CTA an SM, which deals itself
+//     items (a pair and a key head), or, where whole items do not come out even, equal runs of the
+//     tiles of all items; an item that several CTAs share is joined by the last of them (a
+//     ticket), in CTA order. More pairs, and each CTA takes one item, the longest first.
 //   * Values of the first and last tile that no row of the item sees are cleared in shared memory
 //     before their MMA (0 x NaN): pages hold anything past the last token.
 //   * Every wait is bounded; a CTA that gives up writes NaN, drains its copies and MMAs and frees
@@ -63,6 +64,31 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Sixteen in place, in one piece: left to itself the compiler follows each with what needs its
+// result and waits for the latency every time.
+__device__ __forceinline__ void ex2_x16(float *y) {
+    asm volatile(
+        "ex2.approx.ftz.f32 %0, %0;\n\t"
+        "ex2.approx.ftz.f32 %1, %1;\n\t"
+        "ex2.approx.ftz.f32 %2, %2;\n\t"
+        "ex2.approx.ftz.f32 %3, %3;\n\t"
+        "ex2.approx.ftz.f32 %4, %4;\n\t"
+        "ex2.approx.ftz.f32 %5, %5;\n\t"
+        "ex2.approx.ftz.f32 %6, %6;\n\t"
+        "ex2.approx.ftz.f32 %7, %7;\n\t"
+        "ex2.approx.ftz.f32 %8, %8;\n\t"
+        "ex2.approx.ftz.f32 %9, %9;\n\t"
+        "ex2.approx.ftz.f32 %10, %10;\n\t"
+        "ex2.approx.ftz.f32 %11, %11;\n\t"
+        "ex2.approx.ftz.f32 %12, %12;\n\t"
+        "ex2.approx.ftz.f32 %13, %13;\n\t"
+        "ex2.approx.ftz.f32 %14, %14;\n\t"
+        "ex2.approx.ftz.f32 %15, %15;\n\t"
+        : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3]), "+f"(y[4]), "+f"(y[5]), "+f"(y[6]),
+          "+f"(y[7]), "+f"(y[8]), "+f"(y[9]), "+f"(y[10]), "+f"(y[11]), "+f"(y[12]), "+f"(y[13]),
+          "+f"(y[14]), "+f"(y[15]));
 }
 
 // Makes the 32 registers of a tensor-memory load depend on the wait that came before.
@@ -139,13 +165,16 @@ __device__ __forceinline__ TileRange pair_tiles(const SeqInfo &s, const AttnArgs
     return r;
 }
 
+// The k-th whole item of CTA c: there and back again.
+__device__ __forceinline__ int item_of(int k, int c, int G) { return k * G + (k & 1 ? G - 1 - c : c); }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const AttnArgs a, int tokens /* of a half */, int listed) {
     using T = TcShape<D>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages], done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, last_s;
@@ -163,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 2; ++e) {
             mbar_init(&q_full[e], 4);
             mbar_init(&s_full[e], 1);
-            mbar_init(&p_full[e], 4);
+            mbar_init(&p_full[e][0], 4);
+            mbar_init(&p_full[e][1], 4);
             mbar_init(&o_full[e], 1);
         }
         for (int i = 0; i < T::kStages; ++i) {
@@ -210,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = b0; b < b1; ++b) mine += pairs_of(b);
     unsigned at = scan(mine, &n_pairs);
     long long begin = 0, end = 0, total = 0;
-    int G = 1, hk_single = 0;
+    int G = 1, hk_single = 0, n_items = 0;
     bool work = true, whole_items = false;
     if (listed) {
         n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
@@ -230,21 +260,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const unsigned before = scan(tiles, &all);
         if (tid <= (int)n_pairs) prefix[tid] = before;
-        unsigned most = __reduce_max_sync(0xFFFFFFFFu, tiles);
+        __syncthreads();
+        total = (long long)all * a.kv_heads;
+        // Whole items, the last pairs of a sequence (which see the most keys) first and the order of
+        // the CTAs turned round every time; or, where the longest share of that is too long, equal
+        // runs of tiles joined where they meet.
+        n_items = (int)n_pairs * a.kv_heads;
+        G = gridDim.x;
+        unsigned most = 0;
+        if (tid < G) {
+            for (int k = 0; k * G < n_items; ++k) {
+                const int i = item_of(k, tid, G);
+                if (i < n_items) {
+                    const int p = (int)n_pairs - 1 - i / a.kv_heads;
+                    most += prefix[p + 1] - prefix[p];
+                }
+            }
+        }
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
         if (lane == 0) max_s[warp] = most;
         __syncthreads();
         for (int w = 0; w < kThreads / 32; ++w) most = max(most, max_s[w]);
-        total = (long long)all * a.kv_heads;
-        // whole items, dealt out in turn, or equal runs of tiles joined where they meet
-        const int n = (int)n_pairs * a.kv_heads;
-        const long long rounds = (n + gridDim.x - 1) / gridDim.x;
-        whole_items = rounds * most * gridDim.x <= total + (long long)kJoinTiles * gridDim.x;
+        whole_items = (long long)most * G <= total + (long long)kJoinTiles * G;
         if (whole_items) {
-            G = gridDim.x;
-            begin = blockIdx.x, end = n;
-            work = begin < end;
+            end = n_items / G;
+            end += end * G < n_items && item_of((int)end, blockIdx.x, G) < n_items;
+            work = end > 0;
         } else {
-            G = (int)min((long long)gridDim.x, total);
+            G = (int)min((long long)G, total);
             work = (int)blockIdx.x < G;
             if (work) {
                 begin = total * blockIdx.x / G;
@@ -283,15 +326,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             g.next = 1;
             return g;
         }
-        if (whole_items) {  // the last pairs of a sequence see the most keys: they come first
-            const int p = (int)x / a.kv_heads, back = (int)n_pairs - 1 - p;
-            g.hk = (int)x - p * a.kv_heads;
+        if (whole_items) {
+            const int i = item_of((int)x, blockIdx.x, G), p = i / a.kv_heads, back = (int)n_pairs - 1 - p;
+            g.hk = i - p * a.kv_heads;
             g.b = pair_b[back];
             g.s = load_seq(a.m, g.b);
             g.i0 = pair_t[back] * 2 * tokens;
             clip_halves(g, a, tokens, 0, 1 << 30);
             g.first = g.last = 0;
-            g.next = x + G;
+            g.next = x + 1;
             return g;
         }
         const long long head = total / a.kv_heads;
@@ -380,32 +423,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -------------------------------------------------------------------- MMAs
         constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
         constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D) | (1u << 16);  // B is N-major
+        // What the tensor-core instructions take is kept the same in all lanes, and broadcast, so
+        // that it lies in uniform registers: issued from others, one MMA took 110 cycles.
+        auto same = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+        const uint32_t tm = same(tmem), q_desc = same(desc_sw128_low(q_base)), k_desc = same(desc_sw128_low(ring));
+        const uint32_t v_desc = same(desc_sw128_mn_low(ring, kTile * 128));
         int stage = 0;
         uint32_t phase = 0, q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, &abort_flag));
+            if (!__all_sync(0xFFFFFFFFu, mbar_try_parity(bar, parity)))
+                ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, &abort_flag));
             return ok;
         };
         auto scores = [&](int e, int st) {  // S_e = Q_e K^T
-            if (lane == 0) {
+            const uint32_t qd = q_desc + e * (T::kQ >> 4), kd = k_desc + st * (T::kStage >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (uint32_t)(k >> 2) * (kTile * 128) + (k & 3) * 32;
-                    tc_mma_f16(tmem + T::kS0 + e * kTile, smem_desc_sw128(q_base + e * T::kQ + off),
-                               smem_desc_sw128(ring + st * T::kStage + off), idesc_s, k > 0);
+                    const uint32_t off = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
+                    tc_mma_f16(tm + T::kS0 + e * kTile, desc_of(qd + off), desc_of(kd + off), idesc_s, k > 0);
                 }
                 tc_commit(&s_full[e]);
             }
             __syncwarp();
         };
+        auto commit = [&](uint64_t *bar) {
+            if (elect_one()) tc_commit(bar);
+            __syncwarp();
+        };
         for (long long x = begin; x < end && ok;) {
             const Segment g = segment(x);
             x = g.next;
-            if (g.jb <= g.ja) continue;
+            const int ja = same(g.ja), jb = same(g.jb), lo = same(g.lo), hi = same(g.hi);
+            const int ha[2] = {(int)same(g.h[0].a), (int)same(g.h[1].a)}, hb[2] = {(int)same(g.h[0].b), (int)same(g.h[1].b)};
+            if (jb <= ja) continue;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (g.h[e].b > g.h[e].a) {
+                if (hb[e] > ha[e]) {
                     if (!wait(&q_full[e], q_ph[e])) break;
                     q_ph[e] ^= 1u;
                 }
@@ -413,22 +468,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (g.ja >= g.h[e].a && g.ja < g.h[e].b) scores(e, stage);
-            if (lane == 0) tc_commit(&empty[stage]);
-            __syncwarp();
+                if (ja >= ha[e] && ja < hb[e]) scores(e, stage);
+            commit(&empty[stage]);
             if (++stage == T::kStages) stage = 0, phase ^= 1u;
-            for (int j = g.ja; j < g.jb && ok; ++j) {
+            for (int j = ja; j < jb && ok; ++j) {
                 const int vs = stage;
                 const uint32_t vp = phase;
                 if (++stage == T::kStages) stage = 0, phase ^= 1u;
                 const int ks = stage;
                 const uint32_t kp = phase;
-                const bool more = j + 1 < g.jb;
+                const bool more = j + 1 < jb;
                 if (!wait(&full[vs], vp)) break;
                 const int t0 = j * kTile;
-                if (t0 < g.lo || t0 + kTile > g.hi) {
+                if (t0 < lo || t0 + kTile > hi) {
                     // rows of the tile that no row sees
-                    const int n0 = max(g.lo - t0, 0), n1 = min(g.hi - t0, kTile);
+                    const int n0 = max(lo - t0, 0), n1 = min(hi - t0, kTile);
                     for (int i = lane; i < kTile * T::kHalves * 8; i += 32) {
                         const int row = (i >> 3) & (kTile - 1);
                         if (row < n0 || row >= n1)
@@ -437,38 +491,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
+                const uint32_t vd = v_desc + vs * (T::kStage >> 4);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    if (j >= g.h[e].a && j < g.h[e].b) {
-                        if (!wait(&p_full[e], p_ph[e])) break;
+                    if (j >= ha[e] && j < hb[e]) {
+                        // the first 64 keys as soon as their probabilities are there
+                        if (!wait(&p_full[e][0], p_ph[e])) break;
+                        tc_fence_after();
+                        auto values = [&](int k, uint32_t accumulate) {
+                            tc_mma_f16_ts(tm + T::kO0 + e * kTile, tm + T::kS0 + e * kTile + k * 8,
+                                          desc_of(vd + k * (2048 >> 4)), idesc_o, accumulate);
+                        };
+                        if (elect_one()) {
+                            values(0, j > ha[e]);
+#pragma unroll
+                            for (int k = 1; k < 4; ++k) values(k, 1);
+                        }
+                        __syncwarp();
+                        if (!wait(&p_full[e][1], p_ph[e])) break;
                         p_ph[e] ^= 1u;
                         tc_fence_after();
-                        if (lane == 0) {
+                        if (elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k)
-                                tc_mma_f16_ts(tmem + T::kO0 + e * kTile, tmem + T::kS0 + e * kTile + k * 8,
-                                              smem_desc_sw128_mn(ring + vs * T::kStage + k * 2048, kTile * 128, 1024),
-                                              idesc_o, (j > g.h[e].a) | (k > 0));
-                            if (j + 1 == g.h[e].b) tc_commit(&o_full[e]);
+                            for (int k = 4; k < 8; ++k) values(k, 1);
+                            if (j + 1 == hb[e]) tc_commit(&o_full[e]);
                         }
                         __syncwarp();
                     }
-                    if (e == 1 && lane == 0) tc_commit(&empty[vs]);
-                    __syncwarp();
+                    if (e == 1) commit(&empty[vs]);
                     if (more) {
                         if (e == 0) {
                             if (!wait(&full[ks], kp)) break;
                             tc_fence_after();
                         }
-                        if (j + 1 >= g.h[e].a && j + 1 < g.h[e].b) scores(e, ks);
-                        if (e == 1 && lane == 0) tc_commit(&empty[ks]);
-                        __syncwarp();
+                        if (j + 1 >= ha[e] && j + 1 < hb[e]) scores(e, ks);
+                        if (e == 1) commit(&empty[ks]);
                     }
                 }
                 if (more && ++stage == T::kStages) stage = 0, phase ^= 1u;
             }
         }
-        if (lane == 0) {  // nothing may be in flight when the memory is given back
+        if (elect_one()) {  // nothing may be in flight when the memory is given back
             tc_commit(&done);
             wait_hw(&done, 0);
         }
@@ -529,35 +592,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (dead) break;
                 s_ph ^= 1u;
                 tc_fence_after();
-                // All of the row for its maximum. The second half is read again for the exponentials:
-                // kept, the row and what the rest needs would not fit the registers.
-                uint32_t s01[64];
+                // The row is read twice, for its maximum and for the exponentials: tensor memory
+                // is near, and a row kept in registers leaves too few for the rest (what spills
+                // goes to L2, the shared memory has all of the L1).
                 // columns [c0, c1) are visible; all of them inside the range that every row sees
                 const int t0 = j * kTile, c0 = lo - t0, c1 = hi - t0;
                 const bool masked = t0 < in_lo || t0 + kTile > in_hi;
+                uint32_t u0[32], u1[32];
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                {
-                    uint32_t s23[64];
-                    tmem_ld_x32(s_addr, s01);
-                    tmem_ld_x32(s_addr + 32, s01 + 32);
-                    tmem_ld_x32(s_addr + 64, s23);
-                    tmem_ld_x32(s_addr + 96, s23 + 32);
-                    tmem_ld_wait();
-                    pin32(s01), pin32(s01 + 32), pin32(s23), pin32(s23 + 32);
+                auto maxima = [&](const uint32_t *u, int c) {
                     if (masked) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) {
-                            mx[c & 3] = fmaxf(mx[c & 3], c >= c0 && c < c1 ? __uint_as_float(s01[c]) : -INFINITY);
-                            mx[c & 3] = fmaxf(mx[c & 3], c + 64 >= c0 && c + 64 < c1 ? __uint_as_float(s23[c]) : -INFINITY);
-                        }
+                        for (int k = 0; k < 32; ++k)
+                            mx[k & 3] = fmaxf(mx[k & 3], c + k >= c0 && c + k < c1 ? __uint_as_float(u[k]) : -INFINITY);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 4)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s01[c + k])), __uint_as_float(s23[c + k]));
+                        for (int k = 0; k < 32; k += 2)
+                            mx[k >> 1 & 3] = fmaxf(fmaxf(mx[k >> 1 & 3], __uint_as_float(u[k])), __uint_as_float(u[k + 1]));
                     }
-                }
+                };
+                tmem_ld_x32(s_addr, u0);
+                tmem_ld_x32(s_addr + 32, u1);
+                tmem_ld_wait();
+                pin32(u0), pin32(u1);
+                maxima(u0, 0);
+                tmem_ld_x32(s_addr + 64, u0);
+                maxima(u1, 32);
+                tmem_ld_x32(s_addr + 96, u1);
+                tmem_ld_wait();
+                pin32(u0), pin32(u1);
+                maxima(u0, 64), maxima(u1, 96);
                 const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const float top = raw == -INFINITY ? raw : log2_score(raw);
                 // raise the maximum: at the first keys, and when the row has grown by 2^kRaise
@@ -580,46 +644,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float off = m == -INFINITY ? 0.f : -m;
-                // 32 columns of S into 16 of P
-                auto exponentials = [&](uint32_t *su, int c) {
-                    float *s = reinterpret_cast<float *>(su);
+                // 32 exponents into 16 columns of P
+                tmem_ld_x32(s_addr, u0);
+                tmem_ld_x32(s_addr + 32, u1);
+                tmem_ld_x32(s_addr, u0);
+                tmem_ld_x32(s_addr + 32, u1);
+                float2 la = make_float2(0.f, 0.f), lb = la;
+                auto probabilities = [&](float *y, int c) {
                     uint32_t p[16];
-                    if (capped) {
+                    // sixteen at a time, so that their latencies overlap
+                    ex2_x16(y);
+                    ex2_x16(y + 16);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] = log2_score(s[k]) + off;
-                    } else {
+                    for (int k = 0; k < 16; ++k) p[k] = pack_bf16x2(y[2 * k], y[2 * k + 1]);
+                    tmem_st_x16(s_addr + c / 2, p);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        la = fadd2(la, make_float2(y[2 * k], y[2 * k + 1]));
+                        lb = fadd2(lb, make_float2(y[2 * k + 2], y[2 * k + 3]));
+                    }
+                };
+                auto hand_over = [&](int part) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[e][part]);
+                };
+                auto exponentials = [&](uint32_t *u, int c) {
+                    float *y = reinterpret_cast<float *>(u);
+                    if (!capped && !masked) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            const float2 y = ffma2(make_float2(s[k], s[k + 1]), make_float2(mul, mul), make_float2(off, off));
-                            s[k] = y.x, s[k + 1] = y.y;
+                            const float2 v = ffma2(make_float2(y[k], y[k + 1]), make_float2(mul, mul), make_float2(off, off));
+                            y[k] = v.x, y[k + 1] = v.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float v = capped ? log2_score(y[k]) + off : fmaf(y[k], mul, off);
+                            y[k] = c + k < c0 || c + k >= c1 ? -INFINITY : v;
                         }
                     }
-                    if (masked) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (c + k < c0 || c + k >= c1) s[k] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 v = make_float2(ex2(s[2 * k]), ex2(s[2 * k + 1]));
-                        l2 = fadd2(l2, v);
-                        p[k] = pack_bf16x2(v.x, v.y);
-                    }
-                    tmem_st_x16(s_addr + c / 2, p);
+                    probabilities(y, c);
                 };
-                uint32_t s23[64];
-                tmem_ld_x32(s_addr + 64, s23);
-                tmem_ld_x32(s_addr + 96, s23 + 32);
-                exponentials(s01, 0);
-                tmem_ld_wait();  // P's next columns are those of the scores just read
-                pin32(s23), pin32(s23 + 32);
-                exponentials(s01 + 32, 32);
-                exponentials(s23, 64);
-                exponentials(s23 + 32, 96);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[e]);
+                tmem_ld_wait();
+                pin32(u0), pin32(u1);
+                exponentials(u0, 0);
+                tmem_ld_x32(s_addr + 64, u0);
+                exponentials(u1, 32);
+                tmem_ld_x32(s_addr + 96, u1);
+                hand_over(0);
+                tmem_ld_wait();
+                pin32(u0), pin32(u1);
+                exponentials(u0, 64);
+                exponentials(u1, 96);
+                hand_over(1);
+                l2 = fadd2(l2, fadd2(la, lb));
             }
             // ------------------------------------------------------- the run's result
             if (any) {
@@ -773,7 +853,7 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     const long long by_seq = (long long)a.m.batch * ((a.m.max_q + 2 * tokens - 1) / (2 * tokens));
     const long long pairs = by_rows < by_seq ? by_rows : by_seq;
     const int sms = di.sm_count < kAttnMaxCtas ? di.sm_count : kAttnMaxCtas;
-    const bool listed = attn_tc_listed(pairs, a.m.batch, a.kv_heads, sms);
+    const bool listed = attn_tc_listed(pairs, a.m.batch);
     long long grid = pairs * a.kv_heads;
     if (listed) {
         const long long most = grid * ((a.m.capacity + kTile - 1) / kTile > 0 ? (a.m.capacity + kTile - 1) / kTile : 1);

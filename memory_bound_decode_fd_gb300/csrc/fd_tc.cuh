@@ -108,6 +108,18 @@ __device__ __forceinline__ void tc_mma_nvf4(uint32_t d_tmem, uint64_t adesc, uin
         : "memory");
 }
 
+// True in one lane of the (converged) warp, always the same one. A branch on it, unlike one on the
+// lane number, leaves the operands of the tensor-core instructions in it in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes));
+    return yes != 0;
+}
+
 // One arrival on `bar` once every tcgen05.mma this thread issued before has completed.
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
     asm volatile(
@@ -211,12 +223,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t sbo
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// The same swizzle for an operand whose M or N dimension is the contiguous one (64 elements of
-// 16 bits a 128-byte row, one row per K index): `lbo` = byte distance between blocks of 64
-// elements along M or N, `sbo` between groups of 8 K indices.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+// The two words of these descriptors, for kernels that step through operands by adding to the
+// low one (address / 16): K-major with 1024-byte atoms side by side; and the same swizzle for an
+// operand whose M or N dimension is the contiguous one (64 elements of 16 bits a 128-byte row, one
+// row per K index), `lbo` = byte distance between blocks of 64 elements along M or N, 1024 between
+// groups of 8 K indices.
+constexpr uint32_t kDescSw128High = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_sw128_low(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_sw128_mn_low(uint32_t saddr, uint32_t lbo) {
+    return (saddr >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) {
+    return (uint64_t)low | ((uint64_t)kDescSw128High << 32);
 }
 
 // Instruction descriptor of kind::mxf4nvf4: E2M1 A and B (packed FP4), UE4M3 scale
