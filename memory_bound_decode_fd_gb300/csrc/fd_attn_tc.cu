@@ -30,6 +30,7 @@
 //   * Every wait is bounded; a CTA that gives up writes NaN, drains its copies and MMAs and frees
 //     its tensor memory.
 #include <atomic>
+#include <type_traits>
 
 #include "fd_attn.h"
 #include "fd_tc.cuh"
@@ -46,8 +47,9 @@ constexpr int kThreads = 384;          // the third group: MMA warp, copy warp, 
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMaxListed = kAttnTcListed;  // q tiles of one list
 constexpr float kRaise = 8.f;        // log2 units
-// What joining the parts of an item costs, in tiles.
-constexpr int kJoinTiles = 6;
+// What beginning an item costs (its queries loaded, the last result written), and what joining the
+// parts of one costs, in tiles.
+constexpr int kItemTiles = 2, kJoinTiles = 6;
 
 template <int D>
 struct TcShape {
@@ -66,35 +68,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Sixteen in place, in one piece: left to itself the compiler follows each with what needs its
-// result and waits for the latency every time.
-__device__ __forceinline__ void ex2_x16(float *y) {
-    asm volatile(
-        "ex2.approx.ftz.f32 %0, %0;\n\t"
-        "ex2.approx.ftz.f32 %1, %1;\n\t"
-        "ex2.approx.ftz.f32 %2, %2;\n\t"
-        "ex2.approx.ftz.f32 %3, %3;\n\t"
-        "ex2.approx.ftz.f32 %4, %4;\n\t"
-        "ex2.approx.ftz.f32 %5, %5;\n\t"
-        "ex2.approx.ftz.f32 %6, %6;\n\t"
-        "ex2.approx.ftz.f32 %7, %7;\n\t"
-        "ex2.approx.ftz.f32 %8, %8;\n\t"
-        "ex2.approx.ftz.f32 %9, %9;\n\t"
-        "ex2.approx.ftz.f32 %10, %10;\n\t"
-        "ex2.approx.ftz.f32 %11, %11;\n\t"
-        "ex2.approx.ftz.f32 %12, %12;\n\t"
-        "ex2.approx.ftz.f32 %13, %13;\n\t"
-        "ex2.approx.ftz.f32 %14, %14;\n\t"
-        "ex2.approx.ftz.f32 %15, %15;\n\t"
-        : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3]), "+f"(y[4]), "+f"(y[5]), "+f"(y[6]),
-          "+f"(y[7]), "+f"(y[8]), "+f"(y[9]), "+f"(y[10]), "+f"(y[11]), "+f"(y[12]), "+f"(y[13]),
-          "+f"(y[14]), "+f"(y[15]));
-}
-
-// Makes the 32 registers of a tensor-memory load depend on the wait that came before.
-__device__ __forceinline__ void pin32(uint32_t *r) {
+// Makes the registers of a tensor-memory load depend on the wait that came before.
+template <int N>
+__device__ __forceinline__ void pin(uint32_t *r) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // Bounded wait that ignores the abort flag (copies landing, MMAs completing).
@@ -129,6 +107,16 @@ __device__ __forceinline__ TileRange tiles_of(const SeqInfo &s, const AttnArgs &
     if (i1 < i0 || hi <= lo) return {0, 0};
     return {lo / kTile, (hi + kTile - 1) / kTile};
 }
+
+// What a CTA does.
+struct Deal {
+    long long begin, end;  // of the list, or rounds of whole items
+    long long total;       // the list's length: every item's tiles and kItemTiles more
+    int G;                 // CTAs that work
+    int n_pairs;
+    bool whole;            // items, not runs of the list
+    int b, t, hk;          // the one item of a CTA without a list
+};
 
 // One run of tiles of one item (pair of halves, key head).
 struct Segment {
@@ -168,6 +156,12 @@ __device__ __forceinline__ TileRange pair_tiles(const SeqInfo &s, const AttnArgs
 // The k-th whole item of CTA c: there and back again.
 __device__ __forceinline__ int item_of(int k, int c, int G) { return k * G + (k & 1 ? G - 1 - c : c); }
 
+// What the softmax warps need at the end of a run.
+struct RunEnd {
+    long long next, row0;  // the next run, and the activation row of the pair's first token
+    int rows, hk, first, last;
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -178,10 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages], done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, last_s;
-    __shared__ int pick_b, pick_t;
+    __shared__ Deal deal;
     __shared__ unsigned scan_s[kThreads / 32], max_s[kThreads / 32];
     __shared__ unsigned prefix[kMaxListed + 1];       // tiles of one key head before each pair
     __shared__ unsigned char pair_b[kMaxListed], pair_t[kMaxListed];
+    __shared__ RunEnd run_end[8][2];
     unsigned char *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     const uint32_t q_base = smem_u32(smem), ring = q_base + 2 * T::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -202,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&done, 1);
         abort_flag = 0;
-        pick_b = -1;
+        deal.begin = deal.end = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -239,9 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned mine = 0, n_pairs;
     for (int b = b0; b < b1; ++b) mine += pairs_of(b);
     unsigned at = scan(mine, &n_pairs);
-    long long begin = 0, end = 0, total = 0;
-    int G = 1, hk_single = 0, n_items = 0;
-    bool work = true, whole_items = false;
     if (listed) {
         n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
         // one list: key head by key head, pair by pair, tile by tile
@@ -253,20 +245,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncthreads();
-        unsigned tiles = 0, all;
+        unsigned cost = 0, all;
         if (tid < (int)n_pairs) {
             const TileRange r = pair_tiles(load_seq(a.m, pair_b[tid]), a, pair_t[tid] * 2 * tokens, tokens);
-            tiles = r.b - r.a;
+            cost = r.b - r.a + kItemTiles;
         }
-        const unsigned before = scan(tiles, &all);
+        const unsigned before = scan(cost, &all);
         if (tid <= (int)n_pairs) prefix[tid] = before;
         __syncthreads();
-        total = (long long)all * a.kv_heads;
+        const long long total = (long long)all * a.kv_heads;
         // Whole items, the last pairs of a sequence (which see the most keys) first and the order of
         // the CTAs turned round every time; or, where the longest share of that is too long, equal
-        // runs of tiles joined where they meet.
-        n_items = (int)n_pairs * a.kv_heads;
-        G = gridDim.x;
+        // runs of the list, joined where they meet.
+        const int n_items = (int)n_pairs * a.kv_heads;
+        int G = gridDim.x;
         unsigned most = 0;
         if (tid < G) {
             for (int k = 0; k * G < n_items; ++k) {
@@ -280,68 +272,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         most = __reduce_max_sync(0xFFFFFFFFu, most);
         if (lane == 0) max_s[warp] = most;
         __syncthreads();
-        for (int w = 0; w < kThreads / 32; ++w) most = max(most, max_s[w]);
-        whole_items = (long long)most * G <= total + (long long)kJoinTiles * G;
-        if (whole_items) {
-            end = n_items / G;
-            end += end * G < n_items && item_of((int)end, blockIdx.x, G) < n_items;
-            work = end > 0;
-        } else {
-            G = (int)min((long long)G, total);
-            work = (int)blockIdx.x < G;
-            if (work) {
-                begin = total * blockIdx.x / G;
-                end = total * (blockIdx.x + 1) / G;
+        if (tid == 0) {
+            for (int w = 0; w < kThreads / 32; ++w) most = max(most, max_s[w]);
+            const bool whole = (long long)most * G <= total + (long long)kJoinTiles * G;
+            const int c = blockIdx.x;
+            if (whole) {
+                deal.end = n_items / G;
+                if (deal.end * G < n_items && item_of((int)deal.end, c, G) < n_items) ++deal.end;
+            } else {
+                G = (int)min((long long)G, total);
+                if (c < G) deal.begin = total * c / G, deal.end = total * (c + 1) / G;
             }
+            deal.whole = whole, deal.G = G, deal.total = total, deal.n_pairs = (int)n_pairs;
         }
     } else {
         // one item: the last pairs of a sequence see the most keys, so they come first
-        hk_single = blockIdx.x % a.kv_heads;
         const int back = blockIdx.x / a.kv_heads;
-        work = back < (int)n_pairs;
         const unsigned want = n_pairs - 1 - back;
-        if (work && at <= want && want < at + mine) {
+        if (back < (int)n_pairs && at <= want && want < at + mine) {
             unsigned left = want - at;
             int b = b0;
             for (unsigned n; left >= (n = pairs_of(b)); ++b) left -= n;
-            pick_b = b;
-            pick_t = (int)left;
+            deal.b = b, deal.t = (int)left, deal.hk = blockIdx.x % a.kv_heads;
+            deal.end = 1;
         }
-        end = 1;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    if (!work) end = begin;
 
     auto segment = [&](long long x) {
         Segment g;
-        if (!listed) {
-            g.b = pick_b, g.hk = hk_single;
+        int t;
+        if (!listed || deal.whole) {
+            if (!listed) {
+                g.b = deal.b, g.hk = deal.hk, t = deal.t;
+            } else {
+                const int i = item_of((int)x, blockIdx.x, deal.G), p = i / a.kv_heads;
+                const int back = deal.n_pairs - 1 - p;
+                g.hk = i - p * a.kv_heads, g.b = pair_b[back], t = pair_t[back];
+            }
             g.s = load_seq(a.m, g.b);
-            g.i0 = pick_t * 2 * tokens;
-            clip_halves(g, a, tokens, 0, 1 << 30);
-            g.first = g.last = 0;
-            g.next = 1;
-            return g;
-        }
-        if (whole_items) {
-            const int i = item_of((int)x, blockIdx.x, G), p = i / a.kv_heads, back = (int)n_pairs - 1 - p;
-            g.hk = i - p * a.kv_heads;
-            g.b = pair_b[back];
-            g.s = load_seq(a.m, g.b);
-            g.i0 = pair_t[back] * 2 * tokens;
+            g.i0 = t * 2 * tokens;
             clip_halves(g, a, tokens, 0, 1 << 30);
             g.first = g.last = 0;
             g.next = x + 1;
             return g;
         }
-        const long long head = total / a.kv_heads;
+        const long long head = deal.total / a.kv_heads;
         g.hk = (int)(x / head);
         const unsigned in_head = (unsigned)(x - g.hk * head);
         int p = 0;
-        for (int up = (int)n_pairs - 1; p < up;) {  // the last pair with prefix[p] <= in_head
+        for (int up = deal.n_pairs - 1; p < up;) {  // the last pair with prefix[p] <= in_head
             const int mid = (p + up + 1) >> 1;
             if (prefix[mid] <= in_head)
                 p = mid;
@@ -353,10 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         g.i0 = pair_t[p] * 2 * tokens;
         const long long item0 = g.hk * head + prefix[p], item1 = g.hk * head + prefix[p + 1];
         const TileRange r = pair_tiles(g.s, a, g.i0, tokens);
-        const long long stop = min(item1, end);
-        clip_halves(g, a, tokens, r.a + (int)(x - item0), r.a + (int)(stop - item0));
-        g.first = (int)(((item0 + 1) * G - 1) / total);
-        g.last = (int)((item1 * G - 1) / total);
+        const long long stop = min(item1, deal.end);
+        // the run's share of the item's tiles
+        const long long nt = r.b - r.a, cost = item1 - item0;
+        clip_halves(g, a, tokens, r.a + (int)((x - item0) * nt / cost), r.a + (int)((stop - item0) * nt / cost));
+        g.first = (int)(((item0 + 1) * deal.G - 1) / deal.total);
+        g.last = (int)((item1 * deal.G - 1) / deal.total);
         g.next = stop;
         return g;
     };
@@ -374,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0, issued = 0;
         bool ok = true;
-        for (long long x = begin; x < end && ok;) {
+        for (long long x = deal.begin; x < deal.end && ok;) {
             const Segment g = segment(x);
             x = g.next;
             auto page_of = [&](int j) {
@@ -452,23 +437,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) tc_commit(bar);
             __syncwarp();
         };
-        for (long long x = begin; x < end && ok;) {
+        for (long long x = deal.begin; x < deal.end && ok;) {
             const Segment g = segment(x);
             x = g.next;
             const int ja = same(g.ja), jb = same(g.jb), lo = same(g.lo), hi = same(g.hi);
             const int ha[2] = {(int)same(g.h[0].a), (int)same(g.h[1].a)}, hb[2] = {(int)same(g.h[0].b), (int)same(g.h[1].b)};
             if (jb <= ja) continue;
+            if (!wait(&full[stage], phase)) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (hb[e] > ha[e]) {
                     if (!wait(&q_full[e], q_ph[e])) break;
                     q_ph[e] ^= 1u;
+                    tc_fence_after();
+                    if (ja >= ha[e]) scores(e, stage);
                 }
-            if (!ok || !wait(&full[stage], phase)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (ja >= ha[e] && ja < hb[e]) scores(e, stage);
+            if (!ok) break;
             commit(&empty[stage]);
             if (++stage == T::kStages) stage = 0, phase ^= 1u;
             for (int j = ja; j < jb && ok; ++j) {
@@ -558,36 +542,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_ph = 0, o_ph = 0;
         bool dead = false;
         constexpr int kSlot = tc_slot_words(D);
-        for (long long x = begin; x < end;) {
+        // What the end of a run needs is kept in shared memory: registers are short in its loop.
+        volatile RunEnd *const ends = run_end[warp];
+        int ja = 0, jb = 0, lo = 0, hi = 0, in_lo = 0, in_hi = 0;
+        constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;  // of a row of Q in 16-byte loads
+        uint4 q_next[D / 8];
+        // Takes up the run at x: its tiles and visible keys for this row, and the row of Q.
+        auto enter = [&](long long x, int which) {
             const Segment g = segment(x);
-            x = g.next;
             const int tl = r / a.group;
             const int i = g.i0 + e * tokens + tl;
             const int h = g.hk * a.group + r - tl * a.group;
             const bool live = tl < tokens && i < g.s.rows;
-            const TileRange jr = e ? g.h[1] : g.h[0];
-            const bool any = jr.b > jr.a;
-            const int hi = live ? key_hi(g.s, i, a.causal) : 0, lo = live ? key_lo(g.s, i, a.window) : 0;
+            ja = e ? g.h[1].a : g.h[0].a, jb = e ? g.h[1].b : g.h[0].b;
+            hi = live ? key_hi(g.s, i, a.causal) : 0, lo = live ? key_lo(g.s, i, a.window) : 0;
             const int i_first = g.i0 + e * tokens, i_last = min(g.s.rows, i_first + tokens) - 1;
-            const int in_hi = key_hi(g.s, i_first, a.causal), in_lo = key_lo(g.s, i_last, a.window);
-            if (any) {
-                // this row of Q into the swizzled tile (rows without a token: zeros)
-                const uint16_t *q = a.q.p + (long long)(g.s.q0 + i) * a.q.ts + h * a.q.hs;
-                const uint32_t dst = q_base + e * T::kQ + r * 128;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 v = live ? *reinterpret_cast<const uint4 *>(q + c * 8) : make_uint4(0, 0, 0, 0);
-                    v.x = and_xor(v.x, q_and, q_xor), v.y = and_xor(v.y, q_and, q_xor);
-                    v.z = and_xor(v.z, q_and, q_xor), v.w = and_xor(v.w, q_and, q_xor);
-                    sts_v4(dst + (c >> 3) * (kTile * 128) + (((c & 7) ^ (r & 7)) << 4), v);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[e]);
+            in_hi = key_hi(g.s, i_first, a.causal), in_lo = key_lo(g.s, i_last, a.window);
+            if (lane == 0) {
+                volatile RunEnd &t = ends[which];
+                t.next = g.next, t.row0 = g.s.q0 + g.i0, t.rows = g.s.rows - g.i0, t.hk = g.hk;
+                t.first = g.first, t.last = g.last;
             }
+            if (jb > ja) {
+                // the warp's 32 rows together, so that a load covers whole rows
+                const long long at = live ? (long long)(g.s.q0 + i) * a.q.ts + h * a.q.hs : 0;
+                const uint32_t rows = __ballot_sync(0xFFFFFFFFu, live);
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    const int row = n * kRowsAtOnce + lane / kLanes;
+                    const long long from = __shfl_sync(0xFFFFFFFFu, at, row);
+                    q_next[n] = rows >> row & 1
+                        ? *reinterpret_cast<const uint4 *>(a.q.p + from + lane % kLanes * 8) : make_uint4(0, 0, 0, 0);
+                }
+            }
+        };
+        // The rows into the swizzled tile (rows without a token: zeros).
+        auto put_q = [&]() {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                const int row = (warp & 3) * 32 + n * kRowsAtOnce + lane / kLanes, c = lane % kLanes;
+                uint4 v = q_next[n];
+                v.x = and_xor(v.x, q_and, q_xor), v.y = and_xor(v.y, q_and, q_xor);
+                v.z = and_xor(v.z, q_and, q_xor), v.w = and_xor(v.w, q_and, q_xor);
+                sts_v4(q_base + e * T::kQ + row * 128 + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4), v);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[e]);
+        };
+        bool more = deal.begin < deal.end;
+        int run = 0;
+        if (more) {
+            enter(deal.begin, 0);
+            if (jb > ja) put_q();
+        }
+        for (; more; run ^= 1) {
             float m = -INFINITY;  // what the exponentials are taken against, log2 units
             float2 l2 = make_float2(0.f, 0.f);
-            for (int j = jr.a; j < jr.b; ++j) {
+            const bool any = jb > ja;
+            const int j0 = ja;
+            for (int j = ja; j < jb; ++j) {
                 if (!dead) dead = !__all_sync(0xFFFFFFFFu, wait_bounded(&s_full[e], s_ph, &abort_flag));
                 if (dead) break;
                 s_ph ^= 1u;
@@ -614,14 +628,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_x32(s_addr, u0);
                 tmem_ld_x32(s_addr + 32, u1);
                 tmem_ld_wait();
-                pin32(u0), pin32(u1);
+                pin<32>(u0), pin<32>(u1);
                 maxima(u0, 0);
                 tmem_ld_x32(s_addr + 64, u0);
                 maxima(u1, 32);
                 tmem_ld_x32(s_addr + 96, u1);
                 tmem_ld_wait();
-                pin32(u0), pin32(u1);
+                pin<32>(u0), pin<32>(u1);
                 maxima(u0, 64), maxima(u1, 96);
+                tmem_ld_x32(s_addr, u0);
+                tmem_ld_x32(s_addr + 32, u1);
                 const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const float top = raw == -INFINITY ? raw : log2_score(raw);
                 // raise the maximum: at the first keys, and when the row has grown by 2^kRaise
@@ -630,87 +646,108 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float f = m == -INFINITY ? 0.f : ex2(m - up);
                     m = up;
                     l2.x *= f, l2.y *= f;
-                    if (j > jr.a) {
+                    if (j > j0) {
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld_x32(o_addr + c, o);
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld_x16(o_addr + c, o);
                             tmem_ld_wait();
-                            pin32(o);
+                            pin<16>(o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st_x32(o_addr + c, o);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st_x16(o_addr + c, o);
                         }
                     }
                 }
                 const float off = m == -INFINITY ? 0.f : -m;
-                // 32 exponents into 16 columns of P
-                tmem_ld_x32(s_addr, u0);
-                tmem_ld_x32(s_addr + 32, u1);
                 tmem_ld_x32(s_addr, u0);
                 tmem_ld_x32(s_addr + 32, u1);
                 float2 la = make_float2(0.f, 0.f), lb = la;
-                auto probabilities = [&](float *y, int c) {
-                    uint32_t p[16];
-                    // sixteen at a time, so that their latencies overlap
-                    ex2_x16(y);
-                    ex2_x16(y + 16);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) p[k] = pack_bf16x2(y[2 * k], y[2 * k + 1]);
-                    tmem_st_x16(s_addr + c / 2, p);
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        la = fadd2(la, make_float2(y[2 * k], y[2 * k + 1]));
-                        lb = fadd2(lb, make_float2(y[2 * k + 2], y[2 * k + 3]));
-                    }
-                };
                 auto hand_over = [&](int part) {
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[e][part]);
                 };
-                auto exponentials = [&](uint32_t *u, int c) {
-                    float *y = reinterpret_cast<float *>(u);
-                    if (!capped && !masked) {
+                // Groups of 16 columns, one behind the other: the exponentials of a group are issued
+                // between the sums and roundings of the one before, whose results have arrived by
+                // then. Left together the compiler waits for each of them. Scores come in chunks of
+                // 32, the next chunk's load as soon as its registers are free.
+                uint32_t p[16];
+                auto step = [&](auto plain, uint32_t *su, const uint32_t *done, int n) {
+                    float *y = reinterpret_cast<float *>(su);
+                    const float *v = reinterpret_cast<const float *>(done);
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            const float2 v = ffma2(make_float2(y[k], y[k + 1]), make_float2(mul, mul), make_float2(off, off));
-                            y[k] = v.x, y[k + 1] = v.y;
+                    for (int k = 0; k < 16; k += 2) {
+                        if (n < kTile / 16) {
+                            float2 f = make_float2(y[k], y[k + 1]);
+                            if constexpr (decltype(plain)::value) {
+                                f = ffma2(f, make_float2(mul, mul), make_float2(off, off));
+                            } else {
+                                const int c = 16 * n + k;
+                                f.x = c < c0 || c >= c1 ? -INFINITY : log2_score(f.x) + off;
+                                f.y = c + 1 < c0 || c + 1 >= c1 ? -INFINITY : log2_score(f.y) + off;
+                            }
+                            y[k] = ex2(f.x), y[k + 1] = ex2(f.y);
                         }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float v = capped ? log2_score(y[k]) + off : fmaf(y[k], mul, off);
-                            y[k] = c + k < c0 || c + k >= c1 ? -INFINITY : v;
+                        if (n > 0) {
+                            p[((n - 1) & 1) * 8 + k / 2] = pack_bf16x2(v[k], v[k + 1]);
+                            if (k & 2)
+                                lb = fadd2(lb, make_float2(v[k], v[k + 1]));
+                            else
+                                la = fadd2(la, make_float2(v[k], v[k + 1]));
                         }
                     }
-                    probabilities(y, c);
+                    if (n > 0 && (n & 1) == 0) tmem_st_x16(s_addr + 8 * (n - 2), p);
+                };
+                auto steps = [&](auto plain) {
+                    step(plain, u0, u0, 0);
+                    step(plain, u0 + 16, u0, 1);
+                    step(plain, u1, u0 + 16, 2);
+                    tmem_ld_x32(s_addr + 64, u0);
+                    step(plain, u1 + 16, u1, 3);
+                    tmem_ld_wait();
+                    pin<32>(u0);
+                    step(plain, u0, u1 + 16, 4);
+                    tmem_ld_x32(s_addr + 96, u1);
+                    hand_over(0);
+                    step(plain, u0 + 16, u0, 5);
+                    tmem_ld_wait();
+                    pin<32>(u1);
+                    step(plain, u1, u0 + 16, 6);
+                    step(plain, u1 + 16, u1, 7);
+                    step(plain, u1, u1 + 16, 8);
                 };
                 tmem_ld_wait();
-                pin32(u0), pin32(u1);
-                exponentials(u0, 0);
-                tmem_ld_x32(s_addr + 64, u0);
-                exponentials(u1, 32);
-                tmem_ld_x32(s_addr + 96, u1);
-                hand_over(0);
-                tmem_ld_wait();
-                pin32(u0), pin32(u1);
-                exponentials(u0, 64);
-                exponentials(u1, 96);
+                pin<32>(u0), pin<32>(u1);
+                // the common case by itself, without a branch from its first load to its last store
+                if (!capped && !masked)
+                    steps(std::true_type{});
+                else
+                    steps(std::false_type{});
                 hand_over(1);
                 l2 = fadd2(l2, fadd2(la, lb));
             }
             // ------------------------------------------------------- the run's result
+            // The next run's queries are read while the last MMAs end, and given to the MMA warp
+            // before this run's result is written.
+            __syncwarp();
+            const long long next = ends[run].next;
+            more = next < deal.end;
+            if (more) enter(next, run ^ 1);
             if (any) {
                 if (!dead) dead = !__all_sync(0xFFFFFFFFu, wait_bounded(&o_full[e], o_ph, &abort_flag));
                 o_ph ^= 1u;
                 tc_fence_after();
             }
+            if (more && jb > ja) put_q();
             float l = l2.x + l2.y, m2 = m;
             if (dead) l = NAN, m2 = 0.f;
-            const bool whole = g.first == g.last;
-            const long long tok = g.s.q0 + i;
+            const int tl = r / a.group;
+            const int first = ends[run].first, last = ends[run].last, n_tokens = ends[run].rows;
+            const bool whole = first == last, live = tl < tokens && e * tokens + tl < n_tokens;
+            const int h0 = ends[run].hk * a.group, h = h0 + r - tl * a.group;
+            const long long tok0 = ends[run].row0, tok = tok0 + e * tokens + tl;
             if (whole) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 uint16_t *out = a.out.p + tok * a.out.ts + h * a.out.hs;
@@ -720,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (any && !dead) {
                         tmem_ld_x32(o_addr + c, o);
                         tmem_ld_wait();
-                        pin32(o);
+                        pin<32>(o);
                     }
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
@@ -739,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // slot: [D / 4][256 rows] of 4 floats, then (maximum, sum) of each row
                 float *slots = a.partials;
                 const int c = blockIdx.x;
-                float *slot = slots + (size_t)(2 * c + (c == g.first ? 1 : 0)) * kSlot;
+                float *slot = slots + (size_t)(2 * c + (c == first ? 1 : 0)) * kSlot;
                 const int row = e * kTile + r;
 #pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
@@ -747,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (any && !dead) {
                         tmem_ld_x32(o_addr + d, o);
                         tmem_ld_wait();
-                        pin32(o);
+                        pin<32>(o);
                     }
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
@@ -763,16 +800,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __threadfence();
                 named_bar_sync(1, kSoftmax);
                 if (tid == 0) {
-                    const unsigned ticket = atomicAdd(&a.counters[g.first], 1u);
-                    last_s = ticket == (unsigned)(g.last - g.first);
-                    if (last_s) a.counters[g.first] = 0;
+                    const unsigned ticket = atomicAdd(&a.counters[first], 1u);
+                    last_s = ticket == (unsigned)(last - first);
+                    if (last_s) a.counters[first] = 0;
                     __threadfence();
                 }
                 named_bar_sync(1, kSoftmax);
                 if (last_s) {
                     // rows (token, head) of the pair that exist, all (row, 4 elements) over the threads
-                    const int n_rows0 = min(tokens, g.s.rows - g.i0) * a.group;
-                    const int n_rows1 = max(0, min(tokens, g.s.rows - g.i0 - tokens)) * a.group;
+                    const int n_rows0 = min(tokens, n_tokens) * a.group;
+                    const int n_rows1 = max(0, min(tokens, n_tokens - tokens)) * a.group;
                     const int n_rows = n_rows0 + n_rows1;
                     // 32 elements of a row at a time: 8 loads of each part in flight
                     for (int idx = tid; idx < n_rows * (D / 32); idx += kSoftmax) {
@@ -781,18 +818,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int he = rr >= n_rows0;
                         if (he) rr -= n_rows0;
                         const int at_row = he * kTile + rr;
-                        const float *sl = slots + (size_t)(2 * g.first + 1) * kSlot;
+                        const float *sl = slots + (size_t)(2 * first + 1) * kSlot;
                         float M = -INFINITY, L = 0.f;
 #pragma unroll 4
-                        for (int k = g.first; k <= g.last; ++k)
-                            M = fmaxf(M, __ldcg(slots + (size_t)(2 * k + (k == g.first ? 1 : 0)) * kSlot + 2 * kTile * D + 2 * at_row));
+                        for (int k = first; k <= last; ++k)
+                            M = fmaxf(M, __ldcg(slots + (size_t)(2 * k + (k == first ? 1 : 0)) * kSlot + 2 * kTile * D + 2 * at_row));
                         const float base = M == -INFINITY ? 0.f : M;
                         float4 acc[8];
 #pragma unroll
                         for (int q = 0; q < 8; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-                        for (int k = g.first; k <= g.last; ++k) {
-                            if (k > g.first) sl = slots + (size_t)(2 * k) * kSlot;
+                        for (int k = first; k <= last; ++k) {
+                            if (k > first) sl = slots + (size_t)(2 * k) * kSlot;
                             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kTile * D) + at_row);
                             const float f = ex2(ml.x - base);
                             L = fmaf(ml.y, f, L);
@@ -805,8 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const float inv = L == 0.f ? 0.f : 1.f / L;
                         const int tt = rr / a.group;
-                        const int hh = g.hk * a.group + rr - tt * a.group;
-                        const long long to = g.s.q0 + g.i0 + he * tokens + tt;
+                        const int hh = h0 + rr - tt * a.group;
+                        const long long to = tok0 + he * tokens + tt;
                         uint16_t *out = a.out.p + to * a.out.ts + hh * a.out.hs + 4 * d0;
 #pragma unroll
                         for (int q = 0; q < 8; q += 2)
