@@ -39,12 +39,13 @@ namespace fd {
 namespace {
 
 constexpr int kTile = 128;           // keys of a tile, rows of a half
-constexpr int kSoftmax = 256;        // threads of the two softmax groups
-constexpr int kMmaWarp = 8, kCopyWarp = 9;
-constexpr int kThreads = 384;          // the third group: MMA warp, copy warp, two idle
-// Registers: a softmax thread holds a row of S. 384 threads launch with 168 each (64512 in all);
-// 2 x 128 x 208 + 128 x 88 = 64512.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kSoftmax = 512;        // softmax threads: two for each row, half of its columns each
+constexpr int kHalf = kSoftmax / 2;  // of one half
+constexpr int kMmaWarp = 16, kCopyWarp = 17;
+constexpr int kThreads = 640;        // the last four warps: MMA, copies, two idle
+// Registers: 640 threads launch with 96 each (61440 in all); 512 x 104 + 128 x 64 = 61440.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
+static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
 constexpr int kMaxListed = kAttnTcListed;  // q tiles of one list
 constexpr float kRaise = 8.f;        // log2 units
 // What beginning an item costs (its queries loaded, the last result written), and what joining the
@@ -110,12 +111,10 @@ __device__ __forceinline__ TileRange tiles_of(const SeqInfo &s, const AttnArgs &
 
 // What a CTA does.
 struct Deal {
-    long long begin, end;  // of the list, or rounds of whole items
-    long long total;       // the list's length: every item's tiles and kItemTiles more
-    int G;                 // CTAs that work
+    int begin, end;   // of the list, or rounds of whole items
+    int run;          // 0: whole items; else the list is dealt out in runs of this length
     int n_pairs;
-    bool whole;            // items, not runs of the list
-    int b, t, hk;          // the one item of a CTA without a list
+    int b, t, hk;     // the one item of a CTA without a list
 };
 
 // One run of tiles of one item (pair of halves, key head).
@@ -127,7 +126,7 @@ struct Segment {
     TileRange h[2];    // of it, what each half sees
     int lo, hi;        // keys that some row of the pair sees
     int first, last;   // CTAs that share the item
-    long long next;    // tile of the list behind the run
+    int next;          // what comes behind the run
 };
 
 __device__ __forceinline__ void clip_halves(Segment &g, const AttnArgs &a, int tokens, int from, int to) {
@@ -156,11 +155,25 @@ __device__ __forceinline__ TileRange pair_tiles(const SeqInfo &s, const AttnArgs
 // The k-th whole item of CTA c: there and back again.
 __device__ __forceinline__ int item_of(int k, int c, int G) { return k * G + (k & 1 ? G - 1 - c : c); }
 
-// What the softmax warps need at the end of a run.
+// What the softmax warps of a half need at the end of a run.
 struct RunEnd {
-    long long next, row0;  // the next run, and the activation row of the pair's first token
-    int rows, hk, first, last;
+    long long row0;  // activation row of the pair's first token
+    int next, rows, hk, first, last;
 };
+
+// Barrier over `threads` threads that also tells all of them whether `any` held in one.
+__device__ __forceinline__ bool bar_or(int id, int threads, bool any) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %3, 0;\n\t"
+        "barrier.cta.red.or.pred p, %1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"((uint32_t)any)
+        : "memory");
+    return r != 0;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -176,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ unsigned scan_s[kThreads / 32], max_s[kThreads / 32];
     __shared__ unsigned prefix[kMaxListed + 1];       // tiles of one key head before each pair
     __shared__ unsigned char pair_b[kMaxListed], pair_t[kMaxListed];
-    __shared__ RunEnd run_end[8][2];
+    __shared__ RunEnd run_end[2][2], joins[2];
     unsigned char *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     const uint32_t q_base = smem_u32(smem), ring = q_base + 2 * T::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -185,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
         for (int e = 0; e < 2; ++e) {
-            mbar_init(&q_full[e], 4);
+            mbar_init(&q_full[e], 8);
             mbar_init(&s_full[e], 1);
             mbar_init(&p_full[e][0], 4);
             mbar_init(&p_full[e][1], 4);
@@ -237,12 +250,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (listed) {
         n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
         // one list: key head by key head, pair by pair, tile by tile
-        for (int b = b0; b < b1; ++b) {
-            const unsigned n = pairs_of(b);
-            for (unsigned t = 0; t < n && at < kMaxListed; ++t, ++at) {
-                pair_b[at] = (unsigned char)b;
-                pair_t[at] = (unsigned char)t;
+        if (tid < a.m.batch) prefix[tid] = at;  // pairs before sequence tid (per is 1)
+        __syncthreads();
+        if (tid < (int)n_pairs) {
+            int b = 0;
+            for (int up = a.m.batch - 1; b < up;) {  // the last sequence with no more than tid before it
+                const int mid = (b + up + 1) >> 1;
+                if (prefix[mid] <= (unsigned)tid)
+                    b = mid;
+                else
+                    up = mid - 1;
             }
+            pair_b[tid] = (unsigned char)b;
+            pair_t[tid] = (unsigned char)(tid - prefix[b]);
         }
         __syncthreads();
         unsigned cost = 0, all;
@@ -258,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the CTAs turned round every time; or, where the longest share of that is too long, equal
         // runs of the list, joined where they meet.
         const int n_items = (int)n_pairs * a.kv_heads;
-        int G = gridDim.x;
+        const int G = gridDim.x;
         unsigned most = 0;
         if (tid < G) {
             for (int k = 0; k * G < n_items; ++k) {
@@ -274,16 +294,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         if (tid == 0) {
             for (int w = 0; w < kThreads / 32; ++w) most = max(most, max_s[w]);
-            const bool whole = (long long)most * G <= total + (long long)kJoinTiles * G;
             const int c = blockIdx.x;
-            if (whole) {
+            deal.run = 0, deal.n_pairs = (int)n_pairs;
+            if (total >= (1ll << 31) || (long long)most * G <= total + (long long)kJoinTiles * G) {
                 deal.end = n_items / G;
-                if (deal.end * G < n_items && item_of((int)deal.end, c, G) < n_items) ++deal.end;
+                if (deal.end * G < n_items && item_of(deal.end, c, G) < n_items) ++deal.end;
             } else {
-                G = (int)min((long long)G, total);
-                if (c < G) deal.begin = total * c / G, deal.end = total * (c + 1) / G;
+                deal.run = (int)((total + G - 1) / G);
+                const long long begin = (long long)deal.run * c;
+                if (begin < total) deal.begin = (int)begin, deal.end = (int)min(total, begin + deal.run);
             }
-            deal.whole = whole, deal.G = G, deal.total = total, deal.n_pairs = (int)n_pairs;
         }
     } else {
         // one item: the last pairs of a sequence see the most keys, so they come first
@@ -302,14 +322,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    auto segment = [&](long long x) {
+    auto segment = [&](int x) {
         Segment g;
-        int t;
-        if (!listed || deal.whole) {
+        if (!listed || deal.run == 0) {
+            int t;
             if (!listed) {
                 g.b = deal.b, g.hk = deal.hk, t = deal.t;
             } else {
-                const int i = item_of((int)x, blockIdx.x, deal.G), p = i / a.kv_heads;
+                const int i = item_of(x, blockIdx.x, gridDim.x), p = i / a.kv_heads;
                 const int back = deal.n_pairs - 1 - p;
                 g.hk = i - p * a.kv_heads, g.b = pair_b[back], t = pair_t[back];
             }
@@ -320,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             g.next = x + 1;
             return g;
         }
-        const long long head = deal.total / a.kv_heads;
-        g.hk = (int)(x / head);
+        const int head = prefix[deal.n_pairs];
+        g.hk = x / head;
         const unsigned in_head = (unsigned)(x - g.hk * head);
         int p = 0;
         for (int up = deal.n_pairs - 1; p < up;) {  // the last pair with prefix[p] <= in_head
@@ -334,15 +354,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         g.b = pair_b[p];
         g.s = load_seq(a.m, g.b);
         g.i0 = pair_t[p] * 2 * tokens;
-        const long long item0 = g.hk * head + prefix[p], item1 = g.hk * head + prefix[p + 1];
+        const int item0 = g.hk * head + prefix[p], item1 = g.hk * head + prefix[p + 1];
         const TileRange r = pair_tiles(g.s, a, g.i0, tokens);
-        const long long stop = min(item1, deal.end);
-        // the run's share of the item's tiles
-        const long long nt = r.b - r.a, cost = item1 - item0;
-        clip_halves(g, a, tokens, r.a + (int)((x - item0) * nt / cost), r.a + (int)((stop - item0) * nt / cost));
-        g.first = (int)(((item0 + 1) * deal.G - 1) / deal.total);
-        g.last = (int)((item1 * deal.G - 1) / deal.total);
-        g.next = stop;
+        g.next = min(item1, deal.end);
+        // the run's share of the item's tiles: of v steps, kItemTiles in each (item1 - item0) are
+        // what beginning the item costs
+        const int cost = item1 - item0;
+        auto share = [&](int v) { return v - (kItemTiles * v + cost - 1) / cost; };
+        clip_halves(g, a, tokens, r.a + share(x - item0), r.a + share(g.next - item0));
+        g.first = item0 / deal.run;
+        g.last = (item1 - 1) / deal.run;
         return g;
     };
 
@@ -359,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0, issued = 0;
         bool ok = true;
-        for (long long x = deal.begin; x < deal.end && ok;) {
+        for (int x = deal.begin; x < deal.end && ok;) {
             const Segment g = segment(x);
             x = g.next;
             auto page_of = [&](int j) {
@@ -437,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) tc_commit(bar);
             __syncwarp();
         };
-        for (long long x = deal.begin; x < deal.end && ok;) {
+        for (int x = deal.begin; x < deal.end && ok;) {
             const Segment g = segment(x);
             x = g.next;
             const int ja = same(g.ja), jb = same(g.jb), lo = same(g.lo), hi = same(g.hi);
@@ -483,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!wait(&p_full[e][0], p_ph[e])) break;
                         tc_fence_after();
                         auto values = [&](int k, uint32_t accumulate) {
-                            tc_mma_f16_ts(tm + T::kO0 + e * kTile, tm + T::kS0 + e * kTile + k * 8,
+                            tc_mma_f16_ts(tm + T::kO0 + e * kTile, tm + T::kS0 + e * kTile + (k >> 2) * 64 + (k & 3) * 8,
                                           desc_of(vd + k * (2048 >> 4)), idesc_o, accumulate);
                         };
                         if (elect_one()) {
@@ -524,10 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ----------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        const int e = warp >> 2;                     // half
+        // Thread (half e, columns 64 c .. 64 c + 63, row r). The two threads of a row keep the same
+        // maximum; P takes the first 32 columns of each one's scores, O is shared out by columns too.
+        const int e = warp >> 3, cg = warp >> 2 & 1;
         const int r = (warp & 3) * 32 + lane;        // row of the half, TMEM lane
+        const int bar = 2 + e;                       // of the half's threads
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t s_addr = lane_base + T::kS0 + e * kTile, o_addr = lane_base + T::kO0 + e * kTile;
+        const uint32_t s_addr = lane_base + T::kS0 + e * kTile + cg * 64;
+        const uint32_t o_addr = lane_base + T::kO0 + e * kTile + cg * (D / 2);
         // A negative scale is put into Q's signs and a scale of 0 into zeros, so that what follows
         // is monotone in S: the maximum of a row is taken before scale and cap.
         const uint32_t q_and = a.scale == 0.f ? 0u : 0xFFFFFFFFu, q_xor = a.scale < 0.f ? 0x80008000u : 0u;
@@ -543,35 +568,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool dead = false;
         constexpr int kSlot = tc_slot_words(D);
         // What the end of a run needs is kept in shared memory: registers are short in its loop.
-        volatile RunEnd *const ends = run_end[warp];
+        volatile RunEnd *const ends = run_end[e];
         int ja = 0, jb = 0, lo = 0, hi = 0, in_lo = 0, in_hi = 0;
         constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;  // of a row of Q in 16-byte loads
-        uint4 q_next[D / 8];
-        // Takes up the run at x: its tiles and visible keys for this row, and the row of Q.
-        auto enter = [&](long long x, int which) {
+        constexpr int kLoads = 16 / kRowsAtOnce;                  // 16 rows a warp
+        uint4 q_next[kLoads];
+        // Takes up the run at x: its tiles and visible keys for this row, and 16 rows of Q.
+        auto enter = [&](int x, int which) {
             const Segment g = segment(x);
-            const int tl = r / a.group;
-            const int i = g.i0 + e * tokens + tl;
-            const int h = g.hk * a.group + r - tl * a.group;
+            const int i_first = g.i0 + e * tokens, i_last = min(g.s.rows, i_first + tokens) - 1;
+            const int tl = r / a.group, i = i_first + tl;
             const bool live = tl < tokens && i < g.s.rows;
             ja = e ? g.h[1].a : g.h[0].a, jb = e ? g.h[1].b : g.h[0].b;
             hi = live ? key_hi(g.s, i, a.causal) : 0, lo = live ? key_lo(g.s, i, a.window) : 0;
-            const int i_first = g.i0 + e * tokens, i_last = min(g.s.rows, i_first + tokens) - 1;
             in_hi = key_hi(g.s, i_first, a.causal), in_lo = key_lo(g.s, i_last, a.window);
-            if (lane == 0) {
+            if (tid == e * kHalf) {
                 volatile RunEnd &t = ends[which];
                 t.next = g.next, t.row0 = g.s.q0 + g.i0, t.rows = g.s.rows - g.i0, t.hk = g.hk;
                 t.first = g.first, t.last = g.last;
             }
             if (jb > ja) {
-                // the warp's 32 rows together, so that a load covers whole rows
-                const long long at = live ? (long long)(g.s.q0 + i) * a.q.ts + h * a.q.hs : 0;
-                const uint32_t rows = __ballot_sync(0xFFFFFFFFu, live);
+                // whole rows in a load: lane l knows where row (l & 15) of the warp's 16 begins
+                const int row = (warp & 7) * 16 + (lane & 15), t = row / a.group;
+                const bool there = t < tokens && i_first + t < g.s.rows;
+                const long long at = there ? (long long)(g.s.q0 + i_first + t) * a.q.ts +
+                                                 (g.hk * a.group + row - t * a.group) * a.q.hs : 0;
+                const uint32_t rows = __ballot_sync(0xFFFFFFFFu, there);
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    const int row = n * kRowsAtOnce + lane / kLanes;
-                    const long long from = __shfl_sync(0xFFFFFFFFu, at, row);
-                    q_next[n] = rows >> row & 1
+                for (int n = 0; n < kLoads; ++n) {
+                    const int k = n * kRowsAtOnce + lane / kLanes;
+                    const long long from = __shfl_sync(0xFFFFFFFFu, at, k);
+                    q_next[n] = rows >> k & 1
                         ? *reinterpret_cast<const uint4 *>(a.q.p + from + lane % kLanes * 8) : make_uint4(0, 0, 0, 0);
                 }
             }
@@ -579,8 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The rows into the swizzled tile (rows without a token: zeros).
         auto put_q = [&]() {
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-                const int row = (warp & 3) * 32 + n * kRowsAtOnce + lane / kLanes, c = lane % kLanes;
+            for (int n = 0; n < kLoads; ++n) {
+                const int row = (warp & 7) * 16 + n * kRowsAtOnce + lane / kLanes, c = lane % kLanes;
                 uint4 v = q_next[n];
                 v.x = and_xor(v.x, q_and, q_xor), v.y = and_xor(v.y, q_and, q_xor);
                 v.z = and_xor(v.z, q_and, q_xor), v.w = and_xor(v.w, q_and, q_xor);
@@ -591,64 +618,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&q_full[e]);
         };
         bool more = deal.begin < deal.end;
-        int run = 0;
+        int run = 0, n_joins = 0;
         if (more) {
             enter(deal.begin, 0);
             if (jb > ja) put_q();
         }
         for (; more; run ^= 1) {
+            named_bar_sync(bar, kHalf);  // ends[run] is written, ends[run ^ 1] no longer read
             float m = -INFINITY;  // what the exponentials are taken against, log2 units
             float2 l2 = make_float2(0.f, 0.f);
-            const bool any = jb > ja;
+            const bool any = jb > ja && !dead;
             const int j0 = ja;
-            for (int j = ja; j < jb; ++j) {
-                if (!dead) dead = !__all_sync(0xFFFFFFFFu, wait_bounded(&s_full[e], s_ph, &abort_flag));
-                if (dead) break;
+            for (int j = ja; j < jb && !dead; ++j) {
+                const bool ok = __all_sync(0xFFFFFFFFu, wait_bounded(&s_full[e], s_ph, &abort_flag));
                 s_ph ^= 1u;
                 tc_fence_after();
-                // The row is read twice, for its maximum and for the exponentials: tensor memory
-                // is near, and a row kept in registers leaves too few for the rest (what spills
-                // goes to L2, the shared memory has all of the L1).
-                // columns [c0, c1) are visible; all of them inside the range that every row sees
-                const int t0 = j * kTile, c0 = lo - t0, c1 = hi - t0;
-                const bool masked = t0 < in_lo || t0 + kTile > in_hi;
-                uint32_t u0[32], u1[32];
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto maxima = [&](const uint32_t *u, int c) {
-                    if (masked) {
+                // The scores are read twice, for their maximum and for the exponentials: tensor
+                // memory is near, and kept in registers they would leave too few for the rest
+                // (what spills goes to L2, the shared memory has all of the L1).
+                // Columns [c0, c1) of this thread's 64 are visible; all of them inside the range that
+                // every row sees.
+                const int t0 = j * kTile + cg * 64, c0 = lo - t0, c1 = hi - t0;
+                const bool masked = t0 < in_lo || t0 + 64 > in_hi;
+                float top;
+                uint32_t last_score;
+                {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint32_t u[32];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            mx[k & 3] = fmaxf(mx[k & 3], c + k >= c0 && c + k < c1 ? __uint_as_float(u[k]) : -INFINITY);
-                    } else {
+                    for (int c = 0; c < 64; c += 32) {
+                        tmem_ld_x32(s_addr + c, u);
+                        tmem_ld_wait();
+                        pin<32>(u);
+                        if (masked) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-                            mx[k >> 1 & 3] = fmaxf(fmaxf(mx[k >> 1 & 3], __uint_as_float(u[k])), __uint_as_float(u[k + 1]));
+                            for (int k = 0; k < 32; ++k)
+                                mx[k & 3] = fmaxf(mx[k & 3], c + k >= c0 && c + k < c1 ? __uint_as_float(u[k]) : -INFINITY);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2)
+                                mx[k >> 1 & 3] = fmaxf(fmaxf(mx[k >> 1 & 3], __uint_as_float(u[k])), __uint_as_float(u[k + 1]));
+                        }
                     }
-                };
-                tmem_ld_x32(s_addr, u0);
-                tmem_ld_x32(s_addr + 32, u1);
-                tmem_ld_wait();
-                pin<32>(u0), pin<32>(u1);
-                maxima(u0, 0);
-                tmem_ld_x32(s_addr + 64, u0);
-                maxima(u1, 32);
-                tmem_ld_x32(s_addr + 96, u1);
-                tmem_ld_wait();
-                pin<32>(u0), pin<32>(u1);
-                maxima(u0, 64), maxima(u1, 96);
-                tmem_ld_x32(s_addr, u0);
-                tmem_ld_x32(s_addr + 32, u1);
-                const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const float top = raw == -INFINITY ? raw : log2_score(raw);
-                // raise the maximum: at the first keys, and when the row has grown by 2^kRaise
-                if (__any_sync(0xFFFFFFFFu, top > m && (m == -INFINITY || top - m > kRaise))) {
-                    const float up = fmaxf(top, m);
+                    const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    top = raw == -INFINITY ? raw : log2_score(raw);
+                    last_score = u[31];
+                }
+                // Raise the maximum: at the first keys, and when a row has grown by 2^kRaise. All of the
+                // half do it together, or none (and a wait that gave up ends the loop for all).
+                if (bar_or(bar, kHalf, !ok || (top > m && (m == -INFINITY || top - m > kRaise)))) {
+                    if (bar_or(bar, kHalf, !ok)) {
+                        dead = true;
+                        break;
+                    }
+                    // the row's other maximum, by way of this thread's last column
+                    tmem_st_x1(s_addr + 63, __float_as_uint(top));
+                    tmem_st_wait();
+                    tc_fence_before();
+                    named_bar_sync(bar, kHalf);
+                    tc_fence_after();
+                    uint32_t other;
+                    tmem_ld_x1((s_addr ^ 64u) + 63, &other);
+                    tmem_ld_wait();
+                    pin<1>(&other);
+                    tc_fence_before();
+                    named_bar_sync(bar, kHalf);
+                    tc_fence_after();
+                    tmem_st_x1(s_addr + 63, last_score);
+                    tmem_st_wait();
+                    const float up = fmaxf(fmaxf(top, __uint_as_float(other)), m);
                     const float f = m == -INFINITY ? 0.f : ex2(m - up);
                     m = up;
                     l2.x *= f, l2.y *= f;
                     if (j > j0) {
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
+                        for (int c = 0; c < D / 2; c += 16) {
                             uint32_t o[16];
                             tmem_ld_x16(o_addr + c, o);
                             tmem_ld_wait();
@@ -660,26 +704,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float off = m == -INFINITY ? 0.f : -m;
-                tmem_ld_x32(s_addr, u0);
-                tmem_ld_x32(s_addr + 32, u1);
                 float2 la = make_float2(0.f, 0.f), lb = la;
-                auto hand_over = [&](int part) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[e][part]);
-                };
                 // Groups of 16 columns, one behind the other: the exponentials of a group are issued
                 // between the sums and roundings of the one before, whose results have arrived by
-                // then. Left together the compiler waits for each of them. Scores come in chunks of
-                // 32, the next chunk's load as soon as its registers are free.
-                uint32_t p[16];
+                // then. Left together the compiler waits for each of them.
                 auto step = [&](auto plain, uint32_t *su, const uint32_t *done, int n) {
                     float *y = reinterpret_cast<float *>(su);
                     const float *v = reinterpret_cast<const float *>(done);
+                    uint32_t p[8];
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
-                        if (n < kTile / 16) {
+                        if (n < 4) {
                             float2 f = make_float2(y[k], y[k + 1]);
                             if constexpr (decltype(plain)::value) {
                                 f = ffma2(f, make_float2(mul, mul), make_float2(off, off));
@@ -691,173 +726,182 @@ __global__ void __launch_bounds__(kThreads, 1)
                             y[k] = ex2(f.x), y[k + 1] = ex2(f.y);
                         }
                         if (n > 0) {
-                            p[((n - 1) & 1) * 8 + k / 2] = pack_bf16x2(v[k], v[k + 1]);
+                            p[k / 2] = pack_bf16x2(v[k], v[k + 1]);
                             if (k & 2)
                                 lb = fadd2(lb, make_float2(v[k], v[k + 1]));
                             else
                                 la = fadd2(la, make_float2(v[k], v[k + 1]));
                         }
                     }
-                    if (n > 0 && (n & 1) == 0) tmem_st_x16(s_addr + 8 * (n - 2), p);
+                    if (n > 0) tmem_st_x8(s_addr + 8 * (n - 1), p);
                 };
-                auto steps = [&](auto plain) {
-                    step(plain, u0, u0, 0);
-                    step(plain, u0 + 16, u0, 1);
-                    step(plain, u1, u0 + 16, 2);
-                    tmem_ld_x32(s_addr + 64, u0);
-                    step(plain, u1 + 16, u1, 3);
-                    tmem_ld_wait();
-                    pin<32>(u0);
-                    step(plain, u0, u1 + 16, 4);
-                    tmem_ld_x32(s_addr + 96, u1);
-                    hand_over(0);
-                    step(plain, u0 + 16, u0, 5);
-                    tmem_ld_wait();
-                    pin<32>(u1);
-                    step(plain, u1, u0 + 16, 6);
-                    step(plain, u1 + 16, u1, 7);
-                    step(plain, u1, u1 + 16, 8);
-                };
+                uint32_t v0[16], v1[16];
+                tmem_ld_x16(s_addr, v0);
+                tmem_ld_x16(s_addr + 16, v1);
                 tmem_ld_wait();
-                pin<32>(u0), pin<32>(u1);
+                pin<16>(v0), pin<16>(v1);
+                auto steps = [&](auto plain) {
+                    step(plain, v0, v0, 0);
+                    step(plain, v1, v0, 1);
+                    tmem_ld_x16(s_addr + 32, v0);
+                    tmem_ld_wait();
+                    pin<16>(v0);
+                    step(plain, v0, v1, 2);
+                    tmem_ld_x16(s_addr + 48, v1);
+                    tmem_ld_wait();
+                    pin<16>(v1);
+                    step(plain, v1, v0, 3);
+                    step(plain, v1, v1, 4);
+                };
                 // the common case by itself, without a branch from its first load to its last store
                 if (!capped && !masked)
                     steps(std::true_type{});
                 else
                     steps(std::false_type{});
-                hand_over(1);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[e][cg]);
                 l2 = fadd2(l2, fadd2(la, lb));
             }
             // ------------------------------------------------------- the run's result
             // The next run's queries are read while the last MMAs end, and given to the MMA warp
             // before this run's result is written.
-            __syncwarp();
-            const long long next = ends[run].next;
-            more = next < deal.end;
-            if (more) enter(next, run ^ 1);
+            more = ends[run].next < deal.end;
+            if (more) enter(ends[run].next, run ^ 1);
+            float l = l2.x + l2.y;
             if (any) {
-                if (!dead) dead = !__all_sync(0xFFFFFFFFu, wait_bounded(&o_full[e], o_ph, &abort_flag));
+                // the other half of the row's sum, by way of the scores' first columns, now free
+                const bool ok = !dead && __all_sync(0xFFFFFFFFu, wait_bounded(&o_full[e], o_ph, &abort_flag));
                 o_ph ^= 1u;
                 tc_fence_after();
+                tmem_st_x1(s_addr, __float_as_uint(l));
+                tmem_st_wait();
+                tc_fence_before();
+                dead = bar_or(bar, kHalf, !ok);
+                tc_fence_after();
+                uint32_t other;
+                tmem_ld_x1(s_addr ^ 64u, &other);
+                tmem_ld_wait();
+                pin<1>(&other);
+                // the same order of the two in both threads
+                l = cg ? __uint_as_float(other) + l : l + __uint_as_float(other);
+                tc_fence_before();
             }
             if (more && jb > ja) put_q();
-            float l = l2.x + l2.y, m2 = m;
+            float m2 = m;
             if (dead) l = NAN, m2 = 0.f;
             const int tl = r / a.group;
             const int first = ends[run].first, last = ends[run].last, n_tokens = ends[run].rows;
             const bool whole = first == last, live = tl < tokens && e * tokens + tl < n_tokens;
-            const int h0 = ends[run].hk * a.group, h = h0 + r - tl * a.group;
+            const int h = ends[run].hk * a.group + r - tl * a.group;
             const long long tok0 = ends[run].row0, tok = tok0 + e * tokens + tl;
-            if (whole) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint16_t *out = a.out.p + tok * a.out.ts + h * a.out.hs;
+            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            // whole: a row of the result; else of this CTA's slot, [D / 4][256 rows] of 4 floats, then
+            // (maximum, sum) of each row
+            uint16_t *const out = a.out.p + tok * a.out.ts + h * a.out.hs + cg * (D / 2);
+            float *const slot = a.partials + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == first ? 1 : 0)) * kSlot;
+            const int row = e * kTile + r;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    if (any && !dead) {
-                        tmem_ld_x32(o_addr + c, o);
-                        tmem_ld_wait();
-                        pin<32>(o);
-                    }
+            for (int c = 0; c < D / 2; c += 16) {
+                uint32_t o[16];
+                if (any && !dead) {
+                    tmem_ld_x16(o_addr + c, o);
+                    tmem_ld_wait();
+                    pin<16>(o);
+                }
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
+                for (int k = 0; k < 16; ++k) {
+                    const float y = any && !dead && l != 0.f ? __uint_as_float(o[k]) * inv : dead ? NAN : 0.f;
+                    o[k] = __float_as_uint(y);
+                }
+                if (live && whole) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 8) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            const float y0 = __uint_as_float(o[k + 2 * n]) * inv;
-                            const float y1 = __uint_as_float(o[k + 2 * n + 1]) * inv;
-                            w[n] = dead ? 0x7FC07FC0u : l == 0.f ? 0u : pack_bf16x2(y0, y1);
-                        }
-                        if (live) *reinterpret_cast<uint4 *>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int n = 0; n < 4; ++n)
+                            w[n] = pack_bf16x2(__uint_as_float(o[k + 2 * n]), __uint_as_float(o[k + 2 * n + 1]));
+                        *reinterpret_cast<uint4 *>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                }
-                if (live && a.lse) a.lse[tok * a.q_heads + h] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
-            } else {
-                // slot: [D / 4][256 rows] of 4 floats, then (maximum, sum) of each row
-                float *slots = a.partials;
-                const int c = blockIdx.x;
-                float *slot = slots + (size_t)(2 * c + (c == first ? 1 : 0)) * kSlot;
-                const int row = e * kTile + r;
-#pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
-                    uint32_t o[32];
-                    if (any && !dead) {
-                        tmem_ld_x32(o_addr + d, o);
-                        tmem_ld_wait();
-                        pin<32>(o);
-                    }
+                } else if (live) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 v = any && !dead
-                            ? make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
-                                          __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]))
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (live) __stcg(reinterpret_cast<float4 *>(slot) + (d + k) / 4 * (2 * kTile) + row, v);
-                    }
+                    for (int k = 0; k < 16; k += 4)
+                        __stcg(reinterpret_cast<float4 *>(slot) + (cg * (D / 2) + c + k) / 4 * (2 * kTile) + row,
+                               make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                                           __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])));
                 }
-                if (live)
-                    __stcg(reinterpret_cast<float2 *>(slot + 2 * kTile * D) + row, make_float2(m2, l));
-                __threadfence();
-                named_bar_sync(1, kSoftmax);
-                if (tid == 0) {
-                    const unsigned ticket = atomicAdd(&a.counters[first], 1u);
-                    last_s = ticket == (unsigned)(last - first);
-                    if (last_s) a.counters[first] = 0;
-                    __threadfence();
-                }
-                named_bar_sync(1, kSoftmax);
-                if (last_s) {
-                    // rows (token, head) of the pair that exist, all (row, 4 elements) over the threads
-                    const int n_rows0 = min(tokens, n_tokens) * a.group;
-                    const int n_rows1 = max(0, min(tokens, n_tokens - tokens)) * a.group;
-                    const int n_rows = n_rows0 + n_rows1;
-                    // 32 elements of a row at a time: 8 loads of each part in flight
-                    for (int idx = tid; idx < n_rows * (D / 32); idx += kSoftmax) {
-                        const int d0 = idx / n_rows * 8;
-                        int rr = idx % n_rows;
-                        const int he = rr >= n_rows0;
-                        if (he) rr -= n_rows0;
-                        const int at_row = he * kTile + rr;
-                        const float *sl = slots + (size_t)(2 * first + 1) * kSlot;
-                        float M = -INFINITY, L = 0.f;
-#pragma unroll 4
-                        for (int k = first; k <= last; ++k)
-                            M = fmaxf(M, __ldcg(slots + (size_t)(2 * k + (k == first ? 1 : 0)) * kSlot + 2 * kTile * D + 2 * at_row));
-                        const float base = M == -INFINITY ? 0.f : M;
-                        float4 acc[8];
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-                        for (int k = first; k <= last; ++k) {
-                            if (k > first) sl = slots + (size_t)(2 * k) * kSlot;
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kTile * D) + at_row);
-                            const float f = ex2(ml.x - base);
-                            L = fmaf(ml.y, f, L);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(sl) + (d0 + q) * (2 * kTile) + at_row);
-                                acc[q].x = fmaf(v.x, f, acc[q].x), acc[q].y = fmaf(v.y, f, acc[q].y);
-                                acc[q].z = fmaf(v.z, f, acc[q].z), acc[q].w = fmaf(v.w, f, acc[q].w);
-                            }
-                        }
-                        const float inv = L == 0.f ? 0.f : 1.f / L;
-                        const int tt = rr / a.group;
-                        const int hh = h0 + rr - tt * a.group;
-                        const long long to = tok0 + he * tokens + tt;
-                        uint16_t *out = a.out.p + to * a.out.ts + hh * a.out.hs + 4 * d0;
-#pragma unroll
-                        for (int q = 0; q < 8; q += 2)
-                            *reinterpret_cast<uint4 *>(out + 4 * q) = make_uint4(
-                                pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv),
-                                pack_bf16x2(acc[q + 1].x * inv, acc[q + 1].y * inv),
-                                pack_bf16x2(acc[q + 1].z * inv, acc[q + 1].w * inv));
-                        if (d0 == 0 && a.lse)
-                            a.lse[to * a.q_heads + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-                    }
-                }
-                named_bar_sync(1, kSoftmax);
             }
+            if (live && cg == 0) {
+                if (!whole)
+                    __stcg(reinterpret_cast<float2 *>(slot + 2 * kTile * D) + row, make_float2(m2, l));
+                else if (a.lse)
+                    a.lse[tok * a.q_heads + h] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
+            }
+            if (!whole && tid == 0) {  // joined below
+                RunEnd &t = joins[n_joins];
+                t.row0 = tok0, t.rows = n_tokens, t.hk = ends[run].hk, t.first = first, t.last = last;
+            }
+            n_joins += !whole;
             tc_fence_before();  // the loads of O, before the next run's MMAs
+        }
+        // ----------------------------------------- items that this CTA shares with others
+        if (n_joins > 0) __threadfence();
+        for (int n = 0; n < n_joins; ++n) {
+            named_bar_sync(1, kSoftmax);
+            const int first = joins[n].first, last = joins[n].last;
+            if (tid == 0) {
+                const unsigned ticket = atomicAdd(&a.counters[first], 1u);
+                last_s = ticket == (unsigned)(last - first);
+                if (last_s) a.counters[first] = 0;
+                __threadfence();
+            }
+            named_bar_sync(1, kSoftmax);
+            if (!last_s) continue;
+            // rows (token, head) of the pair that exist, 32 elements of one at a time: 8 loads of each
+            // part in flight
+            const int n_rows0 = min(tokens, joins[n].rows) * a.group;
+            const int n_rows = n_rows0 + max(0, min(tokens, joins[n].rows - tokens)) * a.group;
+            for (int idx = tid; idx < n_rows * (D / 32); idx += kSoftmax) {
+                const int d0 = idx / n_rows * 8;
+                int rr = idx % n_rows;
+                const int he = rr >= n_rows0;
+                if (he) rr -= n_rows0;
+                const int at_row = he * kTile + rr;
+                auto slot_of = [&](int k) {
+                    return a.partials + (size_t)(2 * k + (k == first ? 1 : 0)) * kSlot;
+                };
+                float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+                for (int k = first; k <= last; ++k) M = fmaxf(M, __ldcg(slot_of(k) + 2 * kTile * D + 2 * at_row));
+                const float base = M == -INFINITY ? 0.f : M;
+                float4 acc[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = first; k <= last; ++k) {
+                    const float *sl = slot_of(k);
+                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kTile * D) + at_row);
+                    const float f = ex2(ml.x - base);
+                    L = fmaf(ml.y, f, L);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(sl) + (d0 + q) * (2 * kTile) + at_row);
+                        acc[q].x = fmaf(v.x, f, acc[q].x), acc[q].y = fmaf(v.y, f, acc[q].y);
+                        acc[q].z = fmaf(v.z, f, acc[q].z), acc[q].w = fmaf(v.w, f, acc[q].w);
+                    }
+                }
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                const int tt = rr / a.group, hh = joins[n].hk * a.group + rr - tt * a.group;
+                const long long to = joins[n].row0 + he * tokens + tt;
+                uint16_t *out = a.out.p + to * a.out.ts + hh * a.out.hs + 4 * d0;
+#pragma unroll
+                for (int q = 0; q < 8; q += 2)
+                    *reinterpret_cast<uint4 *>(out + 4 * q) = make_uint4(
+                        pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv),
+                        pack_bf16x2(acc[q + 1].x * inv, acc[q + 1].y * inv),
+                        pack_bf16x2(acc[q + 1].z * inv, acc[q + 1].w * inv));
+                if (d0 == 0 && a.lse) a.lse[to * a.q_heads + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            }
         }
     }
     tc_fence_before();
@@ -879,6 +923,11 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     if (err != cudaSuccess) return err;
     const uint64_t bit = 1ull << (dev & 63);
     if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) & bit)) {
+        // the warps' register shares wait for one another if the launch brings fewer
+        cudaFuncAttributes fa;
+        err = cudaFuncGetAttributes(&fa, attn_tc_kernel<D>);
+        if (err != cudaSuccess) return err;
+        if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
         err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    TcShape<D>::kSmem);
         if (err != cudaSuccess) return err;
