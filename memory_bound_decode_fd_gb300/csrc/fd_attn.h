@@ -88,14 +88,9 @@ cudaError_t status_attn_rows(cudaStream_t stream, unsigned *out, bool clear);
 
 // ---- attention of chunks (fd_attn_tc.cu)
 constexpr int kAttnTcTile = 128;    // keys of a tile
-constexpr int kAttnTcListed = 152;  // pairs of halves whose tiles can form one list
+constexpr int kAttnTcListed = 152;  // pairs of halves, and sequences, that a CTA can list
 // fp32 words of a partial result: 256 rows of head_dim, then (maximum, sum) of each
 __host__ __device__ constexpr int tc_slot_words(int d) { return 2 * 128 * (d + 2); }
-// Whether the items fit the list by which a persistent grid deals them out; otherwise one CTA an
-// item.
-inline bool attn_tc_listed(long long pairs, int batch) {
-    return pairs <= kAttnTcListed && batch <= kAttnTcListed;
-}
 cudaError_t launch_attn_tc(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                            cudaStream_t stream);
 cudaError_t status_attn_tc(cudaStream_t stream, unsigned *out, bool clear);

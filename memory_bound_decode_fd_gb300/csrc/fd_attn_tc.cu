@@ -46,7 +46,9 @@ constexpr int kThreads = 640;        // the last four warps: MMA, copies, two id
 // Registers: 640 threads launch with 96 each (61440 in all); 512 x 104 + 128 x 64 = 61440.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
 static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
-constexpr int kMaxListed = kAttnTcListed;  // q tiles of one list
+constexpr int kMaxListed = kAttnTcListed;  // pairs, and sequences, of one list
+// How the work is dealt out (launch_d).
+enum { kOneItem, kListed, kPersistent };
 constexpr float kRaise = 8.f;        // log2 units
 // What beginning an item costs (its queries loaded, the last result written), and what joining the
 // parts of one costs, in tiles.
@@ -97,6 +99,16 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
         }
     }
     return true;
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ unsigned warp_sum_to(unsigned v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += up;
+    }
+    return v;
 }
 
 // Tiles of 128 keys [a, b) that new tokens i0 .. i1 see together (a >= b: none).
@@ -178,17 +190,17 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool any) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                   const AttnArgs a, int tokens /* of a half */, int listed) {
+                   const AttnArgs a, int tokens /* of a half */, int mode) {
     using T = TcShape<D>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages], done;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, last_s;
+    __shared__ int abort_flag, last_s[2];
     __shared__ Deal deal;
-    __shared__ unsigned scan_s[kThreads / 32], max_s[kThreads / 32];
+    __shared__ unsigned scan_s[kThreads / 32];
     __shared__ unsigned prefix[kMaxListed + 1];       // tiles of one key head before each pair
-    __shared__ unsigned char pair_b[kMaxListed], pair_t[kMaxListed];
+    __shared__ unsigned pairs_before[kMaxListed];     // of each sequence
     __shared__ RunEnd run_end[2][2], joins[2];
     unsigned char *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     const uint32_t q_base = smem_u32(smem), ring = q_base + 2 * T::kQ;
@@ -200,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 2; ++e) {
             mbar_init(&q_full[e], 8);
             mbar_init(&s_full[e], 1);
-            mbar_init(&p_full[e][0], 4);
-            mbar_init(&p_full[e][1], 4);
+            mbar_init(&p_full[e][0], 8);
+            mbar_init(&p_full[e][1], 8);
             mbar_init(&o_full[e], 1);
         }
         for (int i = 0; i < T::kStages; ++i) {
@@ -220,118 +232,147 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dep_wait();
     grid_dep_launch();
 
-    // Sum over the block of one value a thread; returns the sum of the threads before this one.
-    auto scan = [&](unsigned v, unsigned *total) {
-        unsigned inc = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += up;
-        }
-        __syncthreads();
-        if (lane == 31) scan_s[warp] = inc;
-        __syncthreads();
-        unsigned before = inc - v;
-        *total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += scan_s[w];
-            *total += scan_s[w];
-        }
-        return before;
-    };
-
     // ---------------------------------------------------------------- what this CTA does
-    const int per = (a.m.batch + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, a.m.batch), b1 = min(b0 + per, a.m.batch);
     auto pairs_of = [&](int b) { return (unsigned)((load_seq(a.m, b).rows + 2 * tokens - 1) / (2 * tokens)); };
-    unsigned mine = 0, n_pairs;
-    for (int b = b0; b < b1; ++b) mine += pairs_of(b);
-    unsigned at = scan(mine, &n_pairs);
-    if (listed) {
-        n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
-        // one list: key head by key head, pair by pair, tile by tile
-        if (tid < a.m.batch) prefix[tid] = at;  // pairs before sequence tid (per is 1)
-        __syncthreads();
-        if (tid < (int)n_pairs) {
-            int b = 0;
-            for (int up = a.m.batch - 1; b < up;) {  // the last sequence with no more than tid before it
-                const int mid = (b + up + 1) >> 1;
-                if (prefix[mid] <= (unsigned)tid)
-                    b = mid;
-                else
-                    up = mid - 1;
-            }
-            pair_b[tid] = (unsigned char)b;
-            pair_t[tid] = (unsigned char)(tid - prefix[b]);
+    // the sequence of pair p
+    auto seq_of = [&](unsigned p) {
+        int b = 0;
+        for (int up = a.m.batch - 1; b < up;) {  // the last one with no more than p pairs before it
+            const int mid = (b + up + 1) >> 1;
+            if (pairs_before[mid] <= p)
+                b = mid;
+            else
+                up = mid - 1;
         }
-        __syncthreads();
-        unsigned cost = 0, all;
-        if (tid < (int)n_pairs) {
-            const TileRange r = pair_tiles(load_seq(a.m, pair_b[tid]), a, pair_t[tid] * 2 * tokens, tokens);
-            cost = r.b - r.a + kItemTiles;
-        }
-        const unsigned before = scan(cost, &all);
-        if (tid <= (int)n_pairs) prefix[tid] = before;
-        __syncthreads();
+        return b;
+    };
+    const int G = gridDim.x;
+    // What this CTA gets, the largest share of whole items being `most`.
+    auto deal_out = [&](unsigned n_pairs, unsigned all, unsigned most) {
         const long long total = (long long)all * a.kv_heads;
-        // Whole items, the last pairs of a sequence (which see the most keys) first and the order of
-        // the CTAs turned round every time; or, where the longest share of that is too long, equal
-        // runs of the list, joined where they meet.
-        const int n_items = (int)n_pairs * a.kv_heads;
-        const int G = gridDim.x;
-        unsigned most = 0;
-        if (tid < G) {
-            for (int k = 0; k * G < n_items; ++k) {
-                const int i = item_of(k, tid, G);
-                if (i < n_items) {
-                    const int p = (int)n_pairs - 1 - i / a.kv_heads;
-                    most += prefix[p + 1] - prefix[p];
-                }
-            }
+        const int n_items = (int)n_pairs * a.kv_heads, c = blockIdx.x;
+        deal.run = 0, deal.n_pairs = (int)n_pairs;
+        if (mode == kPersistent || total >= (1ll << 31) || (long long)most * G <= total + (long long)kJoinTiles * G) {
+            deal.end = n_items / G;
+            if (deal.end * G < n_items && item_of(deal.end, c, G) < n_items) ++deal.end;
+        } else {
+            deal.run = (int)((total + G - 1) / G);
+            const long long begin = (long long)deal.run * c;
+            if (begin < total) deal.begin = (int)begin, deal.end = (int)min(total, begin + deal.run);
         }
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        if (lane == 0) max_s[warp] = most;
+    };
+    if (mode == kOneItem) {
+        // the last pairs of a sequence see the most keys, so they come first
+        const int per = (a.m.batch + kThreads - 1) / kThreads;
+        const int b0 = min(tid * per, a.m.batch), b1 = min(b0 + per, a.m.batch);
+        unsigned mine = 0, total = 0;
+        for (int b = b0; b < b1; ++b) mine += pairs_of(b);
+        unsigned at = warp_sum_to(mine, lane);  // up to this thread's, in its warp
+        if (lane == 31) scan_s[warp] = at;
         __syncthreads();
-        if (tid == 0) {
-            for (int w = 0; w < kThreads / 32; ++w) most = max(most, max_s[w]);
-            const int c = blockIdx.x;
-            deal.run = 0, deal.n_pairs = (int)n_pairs;
-            if (total >= (1ll << 31) || (long long)most * G <= total + (long long)kJoinTiles * G) {
-                deal.end = n_items / G;
-                if (deal.end * G < n_items && item_of(deal.end, c, G) < n_items) ++deal.end;
-            } else {
-                deal.run = (int)((total + G - 1) / G);
-                const long long begin = (long long)deal.run * c;
-                if (begin < total) deal.begin = (int)begin, deal.end = (int)min(total, begin + deal.run);
-            }
+        at -= mine;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) at += scan_s[w];
+            total += scan_s[w];
         }
-    } else {
-        // one item: the last pairs of a sequence see the most keys, so they come first
-        const int back = blockIdx.x / a.kv_heads;
-        const unsigned want = n_pairs - 1 - back;
-        if (back < (int)n_pairs && at <= want && want < at + mine) {
+        const unsigned back = blockIdx.x / a.kv_heads, want = total - 1 - back;
+        if (back < total && at <= want && want < at + mine) {
             unsigned left = want - at;
             int b = b0;
             for (unsigned n; left >= (n = pairs_of(b)); ++b) left -= n;
             deal.b = b, deal.t = (int)left, deal.hk = blockIdx.x % a.kv_heads;
             deal.end = 1;
         }
+    } else if (warp == 0) {
+        // few sequences: one warp makes the list (a barrier costs more than its other lanes bring)
+        constexpr int kEach = (kMaxListed + 31) / 32;
+        unsigned n[kEach], mine = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int b = lane * kEach + k;
+            n[k] = b < a.m.batch ? pairs_of(b) : 0;
+            mine += n[k];
+        }
+        const unsigned upto = warp_sum_to(mine, lane);
+        unsigned n_pairs = __shfl_sync(0xFFFFFFFFu, upto, 31), at = upto - mine;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int b = lane * kEach + k;
+            if (b < a.m.batch) pairs_before[b] = at;
+            at += n[k];
+        }
+        __syncwarp();
+        if (mode == kListed) {
+            n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
+            // one list: key head by key head, pair by pair, tile by tile
+            unsigned most = 0;
+            mine = 0;
+#pragma unroll 1
+            for (int k = 0; k < kEach; ++k) {
+                const unsigned p = lane * kEach + k;
+                unsigned cost = 0;
+                if (p < n_pairs) {
+                    const int b = seq_of(p);
+                    const TileRange r = pair_tiles(load_seq(a.m, b), a, (p - pairs_before[b]) * 2 * tokens, tokens);
+                    cost = r.b - r.a + kItemTiles;
+                    prefix[p] = mine;
+                }
+                mine += cost;
+                most = max(most, cost);
+            }
+            const unsigned sum = warp_sum_to(mine, lane);
+            for (int k = 0; k < kEach; ++k)
+                if (lane * kEach + k < n_pairs) prefix[lane * kEach + k] += sum - mine;
+            const unsigned all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            if (lane == 0) {
+                prefix[n_pairs] = all;
+                deal_out(n_pairs, all, most);
+            }
+        } else if (lane == 0) {
+            deal_out(n_pairs, 0, 0);
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    if (mode == kListed && deal.n_pairs * a.kv_heads > G) {
+        // Several items a CTA: whole items, the last pairs of a sequence (which see the most keys)
+        // first and the order of the CTAs turned round every time; or, where the longest share of
+        // that is too long, equal runs of the list, joined where they meet.
+        const int n_pairs = deal.n_pairs, n_items = n_pairs * a.kv_heads;
+        unsigned most = 0;
+        if (tid < G) {
+            for (int k = 0; k * G < n_items; ++k) {
+                const int i = item_of(k, tid, G);
+                if (i < n_items) {
+                    const int p = n_pairs - 1 - i / a.kv_heads;
+                    most += prefix[p + 1] - prefix[p];
+                }
+            }
+        }
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        if (lane == 0) scan_s[warp] = most;
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 0; w < kThreads / 32; ++w) most = max(most, scan_s[w]);
+            deal.begin = deal.end = 0;
+            deal_out(n_pairs, prefix[n_pairs], most);
+        }
+        __syncthreads();
+    }
 
     auto segment = [&](int x) {
         Segment g;
-        if (!listed || deal.run == 0) {
+        if (mode == kOneItem || deal.run == 0) {
             int t;
-            if (!listed) {
+            if (mode == kOneItem) {
                 g.b = deal.b, g.hk = deal.hk, t = deal.t;
             } else {
-                const int i = item_of(x, blockIdx.x, gridDim.x), p = i / a.kv_heads;
-                const int back = deal.n_pairs - 1 - p;
-                g.hk = i - p * a.kv_heads, g.b = pair_b[back], t = pair_t[back];
+                const int i = item_of(x, blockIdx.x, G), p = i / a.kv_heads;
+                const unsigned pair = deal.n_pairs - 1 - p;
+                g.hk = i - p * a.kv_heads, g.b = seq_of(pair), t = (int)(pair - pairs_before[g.b]);
             }
             g.s = load_seq(a.m, g.b);
             g.i0 = t * 2 * tokens;
@@ -351,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
                 up = mid - 1;
         }
-        g.b = pair_b[p];
+        g.b = seq_of(p);
         g.s = load_seq(a.m, g.b);
-        g.i0 = pair_t[p] * 2 * tokens;
+        g.i0 = (int)(p - pairs_before[g.b]) * 2 * tokens;
         const int item0 = g.hk * head + prefix[p], item1 = g.hk * head + prefix[p + 1];
         const TileRange r = pair_tiles(g.s, a, g.i0, tokens);
         g.next = min(item1, deal.end);
@@ -500,25 +541,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (j >= ha[e] && j < hb[e]) {
-                        // the first 64 keys as soon as their probabilities are there
-                        if (!wait(&p_full[e][0], p_ph[e])) break;
-                        tc_fence_after();
-                        auto values = [&](int k, uint32_t accumulate) {
+                        // The first 32 keys of both 64s as soon as their probabilities are there, then
+                        // the other ones.
+                        auto values = [&](int k, uint32_t accumulate) {  // keys 16 k ..
                             tc_mma_f16_ts(tm + T::kO0 + e * kTile, tm + T::kS0 + e * kTile + (k >> 2) * 64 + (k & 3) * 8,
                                           desc_of(vd + k * (2048 >> 4)), idesc_o, accumulate);
                         };
+                        if (!wait(&p_full[e][0], p_ph[e])) break;
+                        tc_fence_after();
                         if (elect_one()) {
                             values(0, j > ha[e]);
-#pragma unroll
-                            for (int k = 1; k < 4; ++k) values(k, 1);
+                            values(1, 1), values(4, 1), values(5, 1);
                         }
                         __syncwarp();
                         if (!wait(&p_full[e][1], p_ph[e])) break;
                         p_ph[e] ^= 1u;
                         tc_fence_after();
                         if (elect_one()) {
-#pragma unroll
-                            for (int k = 4; k < 8; ++k) values(k, 1);
+                            values(2, 1), values(3, 1), values(6, 1), values(7, 1);
                             if (j + 1 == hb[e]) tc_commit(&o_full[e]);
                         }
                         __syncwarp();
@@ -633,36 +673,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool ok = __all_sync(0xFFFFFFFFu, wait_bounded(&s_full[e], s_ph, &abort_flag));
                 s_ph ^= 1u;
                 tc_fence_after();
-                // The scores are read twice, for their maximum and for the exponentials: tensor
-                // memory is near, and kept in registers they would leave too few for the rest
+                // Half of the scores are read twice, for their maximum and for the exponentials: tensor
+                // memory is near, and all kept in registers they would leave too few for the rest
                 // (what spills goes to L2, the shared memory has all of the L1).
                 // Columns [c0, c1) of this thread's 64 are visible; all of them inside the range that
                 // every row sees.
                 const int t0 = j * kTile + cg * 64, c0 = lo - t0, c1 = hi - t0;
                 const bool masked = t0 < in_lo || t0 + 64 > in_hi;
                 float top;
-                uint32_t last_score;
+                uint32_t last_score, v0[16], v1[16];
                 {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    uint32_t u[32];
-#pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        tmem_ld_x32(s_addr + c, u);
-                        tmem_ld_wait();
-                        pin<32>(u);
+                    auto maxima = [&](const uint32_t *u, int c) {
                         if (masked) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
+                            for (int k = 0; k < 16; ++k)
                                 mx[k & 3] = fmaxf(mx[k & 3], c + k >= c0 && c + k < c1 ? __uint_as_float(u[k]) : -INFINITY);
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2)
+                            for (int k = 0; k < 16; k += 2)
                                 mx[k >> 1 & 3] = fmaxf(fmaxf(mx[k >> 1 & 3], __uint_as_float(u[k])), __uint_as_float(u[k + 1]));
                         }
-                    }
+                    };
+                    uint32_t u[32];
+                    tmem_ld_x32(s_addr, u);
+                    tmem_ld_wait();
+                    pin<32>(u);
+                    maxima(u, 0), maxima(u + 16, 16);
+                    tmem_ld_x32(s_addr + 32, u);
+                    tmem_ld_wait();
+                    pin<32>(u);
+                    maxima(u, 32), maxima(u + 16, 48);
+                    last_score = u[31];
                     const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     top = raw == -INFINITY ? raw : log2_score(raw);
-                    last_score = u[31];
                 }
                 // Raise the maximum: at the first keys, and when a row has grown by 2^kRaise. All of the
                 // half do it together, or none (and a wait that gave up ends the loop for all).
@@ -735,11 +779,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (n > 0) tmem_st_x8(s_addr + 8 * (n - 1), p);
                 };
-                uint32_t v0[16], v1[16];
                 tmem_ld_x16(s_addr, v0);
                 tmem_ld_x16(s_addr + 16, v1);
                 tmem_ld_wait();
                 pin<16>(v0), pin<16>(v1);
+                auto hand_over = [&](int part) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[e][part]);
+                };
                 auto steps = [&](auto plain) {
                     step(plain, v0, v0, 0);
                     step(plain, v1, v0, 1);
@@ -748,6 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pin<16>(v0);
                     step(plain, v0, v1, 2);
                     tmem_ld_x16(s_addr + 48, v1);
+                    hand_over(0);
                     tmem_ld_wait();
                     pin<16>(v1);
                     step(plain, v1, v0, 3);
@@ -758,10 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     steps(std::true_type{});
                 else
                     steps(std::false_type{});
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[e][cg]);
+                hand_over(1);
                 l2 = fadd2(l2, fadd2(la, lb));
             }
             // ------------------------------------------------------- the run's result
@@ -846,18 +893,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();  // the loads of O, before the next run's MMAs
         }
         // ----------------------------------------- items that this CTA shares with others
-        if (n_joins > 0) __threadfence();
-        for (int n = 0; n < n_joins; ++n) {
+        if (n_joins > 0) {
+            __threadfence();
             named_bar_sync(1, kSoftmax);
-            const int first = joins[n].first, last = joins[n].last;
-            if (tid == 0) {
+            if (tid < n_joins) {
+                const int first = joins[tid].first;
                 const unsigned ticket = atomicAdd(&a.counters[first], 1u);
-                last_s = ticket == (unsigned)(last - first);
-                if (last_s) a.counters[first] = 0;
+                last_s[tid] = ticket == (unsigned)(joins[tid].last - first);
+                if (last_s[tid]) a.counters[first] = 0;
                 __threadfence();
             }
             named_bar_sync(1, kSoftmax);
-            if (!last_s) continue;
+        }
+        for (int n = 0; n < n_joins; ++n) {
+            if (!last_s[n]) continue;
+            const int first = joins[n].first, last = joins[n].last;
             // rows (token, head) of the pair that exist, 32 elements of one at a time: 8 loads of each
             // part in flight
             const int n_rows0 = min(tokens, joins[n].rows) * a.group;
@@ -939,14 +989,15 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     const long long by_seq = (long long)a.m.batch * ((a.m.max_q + 2 * tokens - 1) / (2 * tokens));
     const long long pairs = by_rows < by_seq ? by_rows : by_seq;
     const int sms = di.sm_count < kAttnMaxCtas ? di.sm_count : kAttnMaxCtas;
-    const bool listed = attn_tc_listed(pairs, a.m.batch);
+    // Few sequences: one CTA an SM, and a list by which the tiles come out even where the pairs are
+    // few too. Many: an item a CTA, in the order in which the hardware finds room.
+    const int mode = a.m.batch > kMaxListed ? kOneItem : pairs > kMaxListed ? kPersistent : kListed;
+    const long long tiles = (a.m.capacity + kTile - 1) / kTile;
     long long grid = pairs * a.kv_heads;
-    if (listed) {
-        const long long most = grid * ((a.m.capacity + kTile - 1) / kTile > 0 ? (a.m.capacity + kTile - 1) / kTile : 1);
-        grid = most < sms ? most : sms;
-    }
+    if (mode == kListed) grid *= tiles > 0 ? tiles : 1;
+    if (mode != kOneItem && grid > sms) grid = sms;
     err = launch_kernel(attn_tc_kernel<D>, dim3((unsigned)grid), dim3(kThreads), (size_t)TcShape<D>::kSmem, stream,
-                        1, mk, mv, a, tokens, (int)listed);
+                        1, mk, mv, a, tokens, mode);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
