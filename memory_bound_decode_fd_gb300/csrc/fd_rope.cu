@@ -4,12 +4,13 @@
 //   (y0, y1) = scale * (x0 cos a - x1 sin a, x0 sin a + x1 cos a),   a = position * inv_freq[i]
 //
 // Bound by memory for long inputs (each element read and written once) and by latency for single
-// tokens. A CTA takes kRopeTokens tokens (one when tokens are few, and then only a part of the
-// heads): its threads first make the cosines and sines of those tokens in shared memory, one
-// (token, pair) each, so that they are computed once for all the heads that share them; then each
-// thread takes units of 16 elements of a head, two 16-byte loads and two 16-byte stores (the unit's
-// two vectors are the partners of each other: adjacent ones for interleaved pairs, rot_dim / 2
-// apart for halves).
+// tokens. Each CTA of a grid that fills the GPU takes an equal run of the tokens, four at a time: its
+// threads make the cosines and sines of the next four in shared memory, one (token, pair) each, so
+// that they are computed once for all the heads that share them, and rotate the present four, in
+// units of 16 elements of a head: two 16-byte loads and two 16-byte stores (the unit's two vectors
+// are the partners of each other: adjacent ones for interleaved pairs, rot_dim / 2 apart for halves).
+// Few tokens: one a CTA, its heads over several, so that a single token's 40 or 48 heads are not
+// one CTA's work.
 //
 // Angle: position * inv_freq grows to 1e6 radians and more, where 32 bits leave nothing of the
 // fraction. inv_freq / (2 pi) is taken in 64-bit floating point, its fraction made a 64-bit
@@ -24,189 +25,244 @@ namespace fd {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;     // tokens of a CTA's pass when there are many
+constexpr int kRopeTokens = 4;     // tokens of a pass
+constexpr int kRopeAhead = 32;     // tokens whose places are looked up together
 constexpr int kUnit = 16;          // elements a thread handles at a time
+constexpr int kRopeCtas = 4;       // CTAs of an SM
 
 __device__ unsigned int g_page_status;
 
-// Rotates packed pairs: word w of x holds (x0, x1) of pair w.
-__device__ __forceinline__ uint32_t rotate_pair(uint32_t x, float2 cs) {
+// Rotates the pair in the two halves of x.
+__device__ __forceinline__ uint32_t rotate_pair(uint32_t x, float c, float s) {
     const float a = bf16lo(x), b = bf16hi(x);
-    return pack_bf16x2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
+    return pack_bf16x2(a * c - b * s, a * s + b * c);
 }
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// What a token's rows go to.
-struct Place {
-    long long k, v;   // element offsets of the token in the cache
-    int state;        // 0: the token belongs to no sequence, 1: no place in the cache, 2: both
+// A token: element offsets of its queries, keys and values, and of where they go.
+struct Token {
+    long long q, k, v, q_to, k_to, v_to;
+    int pos;
+    int state;   // 0: it belongs to no sequence, 1: it has no place in the cache, 2: both
+};
+
+// One unit: where it comes from and goes to.
+struct Unit {
+    const uint16_t *from;
+    uint16_t *to;
+    int e;         // its place in the head; -1: nothing to do
+    bool rotate;
+    int t;         // token of the pass
+    uint4 x, y;
 };
 
 // VEC: head_dim and rot_dim are multiples of 16, so that units of 16 elements never straddle the
 // end of the rotated part and every half begins on 16 bytes. Otherwise pairs one by one.
+// head_magic: ceil(2^32 / units of a head), exact for the at most 3 * 1024 * 16 units of a token.
 template <bool APPEND, bool VEC>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int tile, int units_cta) {
-    extern __shared__ float2 cs[];  // [tile][rot_dim / 2] of (cos, sin) * scale
-    __shared__ Place place[kRopeTokens];
-    __shared__ int pos_s[kRopeTokens];
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
+    rope_kernel(const RopeArgs a, int units_cta, unsigned head_magic) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int half = a.rot_dim >> 1;
+    unsigned long long *const step = reinterpret_cast<unsigned long long *>(smem);  // [half] of a turn
+    // Cosines and sines times scale, 2 x [kRopeTokens][rot_dim]. VEC: as (cos, cos, sin, sin) of two
+    // pairs, the first two pairs of all units, then the second two ..: neighbouring threads read
+    // neighbouring 16 bytes. Otherwise all cosines, then all sines.
+    float *const cs0 = reinterpret_cast<float *>(step + half + (half & 1));
+    __shared__ Token tokens[kRopeAhead];
     __shared__ int seq_s;
     const int tid = threadIdx.x;
-    const int half = a.rot_dim >> 1;
-    const int t0 = blockIdx.x * tile;
-    const int n = min(tile, a.tokens - t0);
+    const int t_begin = (int)((long long)a.tokens * blockIdx.x / gridDim.x);
+    const int t_end = (int)((long long)a.tokens * (blockIdx.x + 1) / gridDim.x);
     grid_dep_wait();
     grid_dep_launch();
 
-    if (APPEND) {
-        // the sequence of the first token: how many sequences end at or before it
-        if (tid == 0) seq_s = 0;
-        __syncthreads();
-        int before = 0;
-        for (int b = tid; b < a.m.batch; b += kRopeThreads) before += a.m.q_start[b + 1] <= t0;
-        before = __reduce_add_sync(0xFFFFFFFFu, before);
-        if ((tid & 31) == 0 && before) atomicAdd(&seq_s, before);
-        __syncthreads();
-        if (tid < n) {
-            const int t = t0 + tid;
-            int b = seq_s;
-            while (b < a.m.batch && a.m.q_start[b + 1] <= t) ++b;
-            Place p{0, 0, 0};
-            int pos = 0;
-            if (b < a.m.batch && a.m.q_start[b] <= t) {
-                const int kv = min(max(a.m.kv_len[b], 0), a.m.capacity);
-                const int first = a.m.q_start[b];
-                const int at = kv - (a.m.q_start[b + 1] - first) + (t - first);
-                pos = at;
-                p.state = 1;
-                if (at >= 0 && at < a.m.capacity) {
-                    const int page = a.m.table[(long long)b * a.m.table_stride + (at >> a.m.page_shift)];
-                    if (page >= 0 && page < a.m.num_pages) {
-                        const int off = at & ((1 << a.m.page_shift) - 1);
-                        p.k = page * a.k_page + off * a.k_out.ts;
-                        p.v = page * a.v_page + off * a.v_out.ts;
-                        p.state = 2;
-                    } else {
-                        atomicOr(&g_page_status, (unsigned)FD_DEVICE_STATUS_BAD_PAGE);
-                    }
-                }
-            }
-            if (a.positions) pos = a.positions[t];
-            place[tid] = p;
-            pos_s[tid] = pos;
-        }
-    } else if (tid < n) {
-        pos_s[tid] = a.positions[t0 + tid];
-    }
-    __syncthreads();
-
-    for (int i = tid; i < n * half; i += kRopeThreads) {
-        const int t = i / half, p = i - t * half;
-        double turns = a.inv_freq[p] * 0.15915494309189533577;  // 1 / (2 pi)
+    for (int i = tid; i < half; i += kRopeThreads) {
+        double turns = a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
         turns -= floor(turns);
-        const unsigned long long step = (unsigned long long)(turns * 18446744073709551616.0);
-        const long long frac = (long long)((unsigned long long)(long long)pos_s[t] * step);
-        float s, c;
-        sincospif((float)frac * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
-        cs[i] = make_float2(c * a.scale, s * a.scale);
+        step[i] = (unsigned long long)(turns * 18446744073709551616.0);
     }
-    __syncthreads();
-
+    // Those of the tokens [first, first + n) of the ones looked up.
+    auto angles = [&](int first, int n, float *cs) {
+        for (int i = tid; i < n * half; i += kRopeThreads) {
+            const int t = i / half, p = i - t * half;
+            const long long frac = (long long)((unsigned long long)(long long)tokens[first + t].pos * step[p]);
+            float s, c;
+            sincospif((float)frac * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
+            float *const to = cs + t * a.rot_dim +
+                              (VEC ? (((p >> 1 & 3) * (half >> 3) + (p >> 3)) << 2) + (p & 1) : p);
+            to[0] = c * a.scale;
+            to[VEC ? 2 : half] = s * a.scale;
+        }
+    };
+    // Source and destination of head h (queries, keys, values) of a token.
+    auto locate = [&](const Token &t, int h, const uint16_t **from, uint16_t **to, bool *rotate) {
+        *rotate = true;
+        if (h < a.q_heads) {
+            *from = a.q.p + t.q + h * a.q.hs;
+            *to = a.q_out.p + t.q_to + h * a.q_out.hs;
+            return !APPEND || t.state != 0;
+        }
+        h -= a.q_heads;
+        if (h < a.k_heads) {
+            *from = a.k.p + t.k + h * a.k.hs;
+            *to = a.k_out.p + t.k_to + h * a.k_out.hs;
+            return !APPEND || t.state == 2;
+        }
+        h -= a.k_heads;
+        *rotate = false;
+        *from = a.v.p + t.v + h * a.v.hs;
+        *to = a.v_out.p + t.v_to + h * a.v_out.hs;
+        return t.state == 2;
+    };
     const int heads = a.q_heads + (APPEND ? 2 : 1) * a.k_heads;
-    if (VEC) {
-        const int per_head = a.head_dim / kUnit;
-        const int u0 = blockIdx.y * units_cta;
-        const int nu = min(units_cta, heads * per_head - u0);
-#pragma unroll 2
-        for (int i = tid; i < n * nu; i += kRopeThreads) {
-            const int t = i / nu, u = u0 + i - t * nu;
-            int h = u / per_head;
-            const int e = (u - h * per_head) * kUnit;  // the unit's place in the head
-            const bool rotate = e < a.rot_dim && h < a.q_heads + a.k_heads;
-            const HeadsView *src, *dst;
-            long long to;
-            if (h < a.q_heads) {
-                src = &a.q, dst = &a.q_out;
-                to = (t0 + t) * dst->ts;
-                if (APPEND && place[t].state == 0) continue;
-            } else if (h < a.q_heads + a.k_heads) {
-                h -= a.q_heads;
-                src = &a.k, dst = &a.k_out;
-                if (APPEND && place[t].state != 2) continue;
-                to = APPEND ? place[t].k : (t0 + t) * dst->ts;
-            } else {
-                h -= a.q_heads + a.k_heads;
-                src = &a.v, dst = &a.v_out;
-                if (place[t].state != 2) continue;
-                to = place[t].v;
-            }
-            const uint16_t *from = src->p + (t0 + t) * src->ts + h * src->hs;
-            uint16_t *out = dst->p + to + h * dst->hs;
-            // halves: elements e/2 .. e/2 + 7 of each half; else 16 adjacent ones
-            const bool halves = rotate && !a.interleaved;
-            const int j0 = halves ? e >> 1 : e, j1 = halves ? (e >> 1) + half : e + 8;
-            uint4 x = *reinterpret_cast<const uint4 *>(from + j0);
-            uint4 y = *reinterpret_cast<const uint4 *>(from + j1);
-            if (rotate) {
-                const float2 *f = cs + t * half + (e >> 1);
-                uint32_t xo[4], yo[4];
-                if (halves) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t xw = word(x, w), yw = word(y, w);
-                        const float2 f0 = f[2 * w], f1 = f[2 * w + 1];
-                        const float a0 = bf16lo(xw), b0 = bf16lo(yw), a1 = bf16hi(xw), b1 = bf16hi(yw);
-                        xo[w] = pack_bf16x2(a0 * f0.x - b0 * f0.y, a1 * f1.x - b1 * f1.y);
-                        yo[w] = pack_bf16x2(a0 * f0.y + b0 * f0.x, a1 * f1.y + b1 * f1.x);
-                    }
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        xo[w] = rotate_pair(word(x, w), f[w]);
-                        yo[w] = rotate_pair(word(y, w), f[w + 4]);
+
+    for (int s0 = t_begin; s0 < t_end; s0 += kRopeAhead) {
+        const int n_ahead = min(kRopeAhead, t_end - s0);
+        __syncthreads();
+        if (APPEND) {
+            // the sequence of the first token: how many sequences end at or before it
+            if (tid == 0) seq_s = 0;
+            __syncthreads();
+            int before = 0;
+            for (int b = tid; b < a.m.batch; b += kRopeThreads) before += a.m.q_start[b + 1] <= s0;
+            before = __reduce_add_sync(0xFFFFFFFFu, before);
+            if ((tid & 31) == 0 && before) atomicAdd(&seq_s, before);
+            __syncthreads();
+            if (tid < n_ahead) {
+                const long long t = s0 + tid;
+                int b = seq_s;
+                while (b < a.m.batch && a.m.q_start[b + 1] <= t) ++b;
+                Token k{t * a.q.ts, t * a.k.ts, t * a.v.ts, t * a.q_out.ts, 0, 0, 0, 0};
+                if (b < a.m.batch && a.m.q_start[b] <= t) {
+                    const int kv = min(max(a.m.kv_len[b], 0), a.m.capacity);
+                    const int first = a.m.q_start[b];
+                    const int at = kv - (a.m.q_start[b + 1] - first) + ((int)t - first);
+                    k.pos = at;
+                    k.state = 1;
+                    if (at >= 0 && at < a.m.capacity) {
+                        const int page = a.m.table[(long long)b * a.m.table_stride + (at >> a.m.page_shift)];
+                        if (page >= 0 && page < a.m.num_pages) {
+                            const int off = at & ((1 << a.m.page_shift) - 1);
+                            k.k_to = page * a.k_page + off * a.k_out.ts;
+                            k.v_to = page * a.v_page + off * a.v_out.ts;
+                            k.state = 2;
+                        } else {
+                            atomicOr(&g_page_status, (unsigned)FD_DEVICE_STATUS_BAD_PAGE);
+                        }
                     }
                 }
-                x = make_uint4(xo[0], xo[1], xo[2], xo[3]);
-                y = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+                if (a.positions) k.pos = a.positions[t];
+                tokens[tid] = k;
             }
-            *reinterpret_cast<uint4 *>(out + j0) = x;
-            *reinterpret_cast<uint4 *>(out + j1) = y;
+        } else if (tid < n_ahead) {
+            const long long t = s0 + tid;
+            tokens[tid] = Token{t * a.q.ts, t * a.k.ts, 0, t * a.q_out.ts, t * a.k_out.ts, 0, a.positions[t], 0};
         }
-    } else {
-        // pairs one by one: head_dim / 2 of them, the rotated ones first
-        const int per_head = a.head_dim / 2;
-        for (int i = tid; i < n * heads * per_head; i += kRopeThreads) {
-            const int t = i / (heads * per_head), r = i - t * heads * per_head;
-            int h = r / per_head;
-            const int p = r - h * per_head;
-            const bool rotate = p < half && h < a.q_heads + a.k_heads;
-            const HeadsView *src, *dst;
-            long long to;
-            if (h < a.q_heads) {
-                src = &a.q, dst = &a.q_out;
-                to = (t0 + t) * dst->ts;
-                if (APPEND && place[t].state == 0) continue;
-            } else if (h < a.q_heads + a.k_heads) {
-                h -= a.q_heads;
-                src = &a.k, dst = &a.k_out;
-                if (APPEND && place[t].state != 2) continue;
-                to = APPEND ? place[t].k : (t0 + t) * dst->ts;
+        __syncthreads();
+        angles(0, min(kRopeTokens, n_ahead), cs0);
+        __syncthreads();
+
+        for (int c = 0; c < n_ahead; c += kRopeTokens) {
+            const int n = min(kRopeTokens, n_ahead - c);
+            const float *const cs = cs0 + (c / kRopeTokens & 1) * kRopeTokens * a.rot_dim;
+            float *const cs_next = cs0 + ((c / kRopeTokens & 1) ^ 1) * kRopeTokens * a.rot_dim;
+            const int n_next = min(kRopeTokens, n_ahead - c - kRopeTokens);  // <= 0: no more
+            if (VEC) {
+                const int per_head = a.head_dim / kUnit;
+                const int u0 = blockIdx.y * units_cta;
+                const int nu = min(units_cta, heads * per_head - u0);
+                auto load = [&](int i, Unit &w) {
+                    w.e = -1;
+                    if (i >= n * nu) return;
+                    w.t = (i >= nu) + (i >= 2 * nu) + (i >= 3 * nu);
+                    const unsigned u = u0 + i - w.t * nu;
+                    const int h = per_head == 1 ? (int)u : (int)__umulhi(u, head_magic);
+                    const int e = (int)u - h * per_head;
+                    if (!locate(tokens[c + w.t], h, &w.from, &w.to, &w.rotate)) return;
+                    w.e = e * kUnit;
+                    w.rotate = w.rotate && w.e < a.rot_dim;
+                    // halves: elements e/2 .. e/2 + 7 of each half; else 16 adjacent ones
+                    const bool halves = w.rotate && !a.interleaved;
+                    const int j0 = halves ? w.e >> 1 : w.e, j1 = halves ? (w.e >> 1) + half : w.e + 8;
+                    w.x = __ldcs(reinterpret_cast<const uint4 *>(w.from + j0));
+                    w.y = __ldcs(reinterpret_cast<const uint4 *>(w.from + j1));
+                };
+                auto store = [&](const Unit &w) {
+                    if (w.e < 0) return;
+                    uint4 x = w.x, y = w.y;
+                    const bool halves = w.rotate && !a.interleaved;
+                    const int j0 = halves ? w.e >> 1 : w.e, j1 = halves ? (w.e >> 1) + half : w.e + 8;
+                    if (w.rotate) {
+                        const float4 *f = reinterpret_cast<const float4 *>(cs + w.t * a.rot_dim) + (w.e >> 4);
+                        uint32_t xo[4], yo[4];
+                        if (halves) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float4 g = f[k * (half >> 3)];
+                                const float2 co = make_float2(g.x, g.y), si = make_float2(g.z, g.w);
+                                const float2 no = make_float2(-g.z, -g.w);
+                                const float2 p = make_float2(bf16lo(word(x, k)), bf16hi(word(x, k)));
+                                const float2 q = make_float2(bf16lo(word(y, k)), bf16hi(word(y, k)));
+                                const float2 zero = make_float2(0.f, 0.f);
+                                const float2 xr = ffma2(p, co, ffma2(q, no, zero));
+                                const float2 yr = ffma2(p, si, ffma2(q, co, zero));
+                                xo[k] = pack_bf16x2(xr.x, xr.y);
+                                yo[k] = pack_bf16x2(yr.x, yr.y);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float4 g = f[k * (half >> 3)];
+                                const uint32_t p0 = k < 2 ? word(x, 2 * k) : word(y, 2 * k - 4);
+                                const uint32_t p1 = k < 2 ? word(x, 2 * k + 1) : word(y, 2 * k - 3);
+                                const uint32_t r0 = rotate_pair(p0, g.x, g.z), r1 = rotate_pair(p1, g.y, g.w);
+                                if (k < 2)
+                                    xo[2 * k] = r0, xo[2 * k + 1] = r1;
+                                else
+                                    yo[2 * k - 4] = r0, yo[2 * k - 3] = r1;
+                            }
+                        }
+                        x = make_uint4(xo[0], xo[1], xo[2], xo[3]);
+                        y = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+                    }
+                    *reinterpret_cast<uint4 *>(w.to + j0) = x;
+                    *reinterpret_cast<uint4 *>(w.to + j1) = y;
+                };
+                Unit w0, w1;
+                load(tid, w0);
+                load(tid + kRopeThreads, w1);
+                if (n_next > 0) angles(c + kRopeTokens, n_next, cs_next);  // while the loads are on their way
+                for (int i = tid; i < n * nu; i += 2 * kRopeThreads) {
+                    store(w0);
+                    store(w1);
+                    load(i + 2 * kRopeThreads, w0);
+                    load(i + 3 * kRopeThreads, w1);
+                }
             } else {
-                h -= a.q_heads + a.k_heads;
-                src = &a.v, dst = &a.v_out;
-                if (place[t].state != 2) continue;
-                to = place[t].v;
+                if (n_next > 0) angles(c + kRopeTokens, n_next, cs_next);
+                // pairs one by one: head_dim / 2 of them, the rotated ones first
+                const int per_head = a.head_dim / 2;
+                for (int i = tid; i < n * heads * per_head; i += kRopeThreads) {
+                    const int t = i / (heads * per_head), r = i - t * heads * per_head;
+                    const int h = r / per_head, p = r - h * per_head;
+                    const uint16_t *from;
+                    uint16_t *to;
+                    bool rotate;
+                    if (!locate(tokens[c + t], h, &from, &to, &rotate)) continue;
+                    rotate = rotate && p < half;
+                    const bool halves = rotate && !a.interleaved;
+                    const int j0 = halves ? p : 2 * p, j1 = halves ? p + half : 2 * p + 1;
+                    uint32_t x = (uint32_t)from[j0] | ((uint32_t)from[j1] << 16);
+                    if (rotate) x = rotate_pair(x, cs[t * a.rot_dim + p], cs[t * a.rot_dim + half + p]);
+                    to[j0] = (uint16_t)x;
+                    to[j1] = (uint16_t)(x >> 16);
+                }
             }
-            const uint16_t *from = src->p + (t0 + t) * src->ts + h * src->hs;
-            uint16_t *out = dst->p + to + h * dst->hs;
-            const bool halves = rotate && !a.interleaved;
-            const int j0 = halves ? p : 2 * p, j1 = halves ? p + half : 2 * p + 1;
-            uint32_t x = (uint32_t)from[j0] | ((uint32_t)from[j1] << 16);
-            if (rotate) x = rotate_pair(x, cs[t * half + p]);
-            out[j0] = (uint16_t)x;
-            out[j1] = (uint16_t)(x >> 16);
+            __syncthreads();
         }
     }
 }
@@ -219,21 +275,21 @@ cudaError_t launch_rope(const RopeArgs &a, bool append, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
     const bool vec = a.head_dim % kUnit == 0 && a.rot_dim % kUnit == 0;
     const int heads = a.q_heads + (append ? 2 : 1) * a.k_heads;
-    // Few tokens: one a CTA, and its units over several CTAs, so that a single token's 40 or 48
-    // heads are not one CTA's work. Many: kRopeTokens a CTA, so that each thread has several
-    // loads in flight and the angles of four tokens keep 256 threads busy.
-    const bool few = a.tokens < 4 * di.sm_count;
-    const int tile = few ? 1 : kRopeTokens;
-    const int units = heads * (a.head_dim / kUnit);
-    int units_cta = units;
-    if (few && vec && units > kRopeThreads) units_cta = kRopeThreads;
-    const int split = vec ? (units + units_cta - 1) / units_cta : 1;
-    const dim3 grid((unsigned)((a.tokens + tile - 1) / tile), (unsigned)split);
-    const size_t smem = (size_t)tile * (a.rot_dim / 2) * sizeof(float2);
-    void (*kern)(const RopeArgs, int, int) =
+    const int per_head = vec ? a.head_dim / kUnit : 1;
+    const int units = heads * per_head;
+    void (*kern)(const RopeArgs, int, unsigned) =
         append ? (vec ? rope_kernel<true, true> : rope_kernel<true, false>)
                : (vec ? rope_kernel<false, true> : rope_kernel<false, false>);
-    err = launch_kernel(kern, grid, dim3(kRopeThreads), smem, stream, 1, a, tile, units_cta);
+    // a run of tokens for each CTA that the GPU holds at a time; few tokens: one a CTA, its units
+    // over several
+    const int most = kRopeCtas * di.sm_count;
+    const int split = vec && a.tokens < 2 * di.sm_count ? (units + kRopeThreads - 1) / kRopeThreads : 1;
+    const int units_cta = (units + split - 1) / split;
+    const dim3 grid((unsigned)(a.tokens < most ? a.tokens : most), (unsigned)split);
+    const size_t smem = (size_t)(a.rot_dim / 2 + 1) * sizeof(unsigned long long) +
+                        (size_t)a.rot_dim * 2 * kRopeTokens * sizeof(float);
+    const unsigned magic = (unsigned)(((1ull << 32) + per_head - 1) / per_head);
+    err = launch_kernel(kern, grid, dim3(kRopeThreads), smem, stream, 1, a, units_cta, magic);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
