@@ -49,6 +49,8 @@ static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kT
 constexpr int kMaxListed = kAttnTcListed;  // pairs, and sequences, of one list
 // How the work is dealt out (launch_d).
 enum { kOneItem, kListed, kPersistent };
+// How scores become exponents (softmax steps).
+enum { kPlain, kSmallCap, kGeneral };
 constexpr float kRaise = 8.f;        // log2 units
 // What beginning an item costs (its queries loaded, the last result written), and what joining the
 // parts of one costs, in tiles.
@@ -69,6 +71,17 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// tanh(y) / y as a polynomial in y^2, for |y| <= 1: the minimax one of degree 7 (found by exchange
+// on a fine grid); with the rounding of its steps tanh(y) is off by at most 1.4 2^-24.
+__device__ __forceinline__ float2 tanh_over(float2 z) {
+    const float c[8] = {1.0f, -0.3333328366f, 0.1333224028f, -0.0538756959f,
+                        0.0214784257f, -0.0079373326f, 0.0022966541f, -0.0003574573f};
+    float2 p = make_float2(c[7], c[7]);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) p = ffma2(p, z, make_float2(c[i], c[i]));
+    return p;
 }
 
 // Makes the registers of a tensor-memory load depend on the wait that came before.
@@ -187,7 +200,8 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool any) {
     return r != 0;
 }
 
-template <int D>
+// CAPPED: the scores go through the tanh (apart, so that its code costs the others no registers).
+template <int D, bool CAPPED>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const AttnArgs a, int tokens /* of a half */, int mode) {
@@ -597,12 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // is monotone in S: the maximum of a row is taken before scale and cap.
         const uint32_t q_and = a.scale == 0.f ? 0u : 0xFFFFFFFFu, q_xor = a.scale < 0.f ? 0x80008000u : 0u;
         const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
-        const bool capped = a.softcap > 0.f;
-        const float mul = capped ? scale / a.softcap * (2.f * kLog2e) : scale * kLog2e;
-        const float cap_out = a.softcap * kLog2e;
+        const float cap_in = CAPPED ? scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+        const float mul = CAPPED ? cap_in * (2.f * kLog2e) : scale * kLog2e;
         // a score in log2 units; c tanh(y) = c (1 - 2 / (e^(2 y) + 1))
         auto log2_score = [&](float v) {
-            return capped ? cap_out - __fdividef(2.f * cap_out, ex2(v * mul) + 1.f) : v * mul;
+            return CAPPED ? cap_out - __fdividef(2.f * cap_out, ex2(v * mul) + 1.f) : v * mul;
         };
         uint32_t s_ph = 0, o_ph = 0;
         bool dead = false;
@@ -680,33 +693,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // every row sees.
                 const int t0 = j * kTile + cg * 64, c0 = lo - t0, c1 = hi - t0;
                 const bool masked = t0 < in_lo || t0 + 64 > in_hi;
-                float top;
+                uint32_t seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // a bit a column
+                if (masked) {
+                    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+                    seen[0] = below(c1) & ~below(c0), seen[1] = below(c1 - 32) & ~below(c0 - 32);
+                }
+                float top, size = 0.f;
                 uint32_t last_score, v0[16], v1[16];
                 {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto maxima = [&](const uint32_t *u, int c) {
+                    uint32_t u[32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tmem_ld_x32(s_addr + 32 * c, u);
+                        tmem_ld_wait();
+                        pin<32>(u);
                         if (masked) {
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                mx[k & 3] = fmaxf(mx[k & 3], c + k >= c0 && c + k < c1 ? __uint_as_float(u[k]) : -INFINITY);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 16; k += 2)
-                                mx[k >> 1 & 3] = fmaxf(fmaxf(mx[k >> 1 & 3], __uint_as_float(u[k])), __uint_as_float(u[k + 1]));
+                            for (int k = 0; k < 32; ++k)
+                                if (!(seen[c] >> k & 1)) u[k] = 0xFF800000u;  // -infinity
                         }
-                    };
-                    uint32_t u[32];
-                    tmem_ld_x32(s_addr, u);
-                    tmem_ld_wait();
-                    pin<32>(u);
-                    maxima(u, 0), maxima(u + 16, 16);
-                    tmem_ld_x32(s_addr + 32, u);
-                    tmem_ld_wait();
-                    pin<32>(u);
-                    maxima(u, 32), maxima(u + 16, 48);
-                    last_score = u[31];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            mx[k >> 1 & 3] = fmaxf(fmaxf(mx[k >> 1 & 3], __uint_as_float(u[k])), __uint_as_float(u[k + 1]));
+                        if (CAPPED) {
+                            // how far from 0 the lowest one is, the hidden ones set aside
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (seen[c] >> k & 1) size = fmaxf(size, -__uint_as_float(u[k]));
+                        }
+                        if (c == 1) last_score = u[31];
+                    }
                     const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     top = raw == -INFINITY ? raw : log2_score(raw);
+                    size = fmaxf(size, raw);
                 }
                 // Raise the maximum: at the first keys, and when a row has grown by 2^kRaise. All of the
                 // half do it together, or none (and a wait that gave up ends the loop for all).
@@ -752,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Groups of 16 columns, one behind the other: the exponentials of a group are issued
                 // between the sums and roundings of the one before, whose results have arrived by
                 // then. Left together the compiler waits for each of them.
-                auto step = [&](auto plain, uint32_t *su, const uint32_t *done, int n) {
+                auto step = [&](auto kind, uint32_t *su, const uint32_t *done, int n) {
                     float *y = reinterpret_cast<float *>(su);
                     const float *v = reinterpret_cast<const float *>(done);
                     uint32_t p[8];
@@ -760,12 +780,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 16; k += 2) {
                         if (n < 4) {
                             float2 f = make_float2(y[k], y[k + 1]);
-                            if constexpr (decltype(plain)::value) {
+                            if constexpr (decltype(kind)::value == kPlain) {
                                 f = ffma2(f, make_float2(mul, mul), make_float2(off, off));
                             } else {
-                                const int c = 16 * n + k;
-                                f.x = c < c0 || c >= c1 ? -INFINITY : log2_score(f.x) + off;
-                                f.y = c + 1 < c0 || c + 1 >= c1 ? -INFINITY : log2_score(f.y) + off;
+                                if constexpr (!CAPPED) {
+                                    f = ffma2(f, make_float2(mul, mul), make_float2(off, off));
+                                } else if constexpr (decltype(kind)::value == kSmallCap) {
+                                    const float2 zero = make_float2(0.f, 0.f);
+                                    f = ffma2(f, make_float2(cap_in, cap_in), zero);
+                                    const float2 t = tanh_over(ffma2(f, f, zero));
+                                    f = ffma2(ffma2(f, make_float2(cap_out, cap_out), zero), t, make_float2(off, off));
+                                } else {
+                                    f.x = log2_score(f.x) + off, f.y = log2_score(f.y) + off;
+                                }
+                                const uint32_t see = seen[(16 * n + k) >> 5] >> ((16 * n + k) & 31);
+                                f.x = see & 1 ? f.x : -INFINITY;
+                                f.y = see & 2 ? f.y : -INFINITY;
                             }
                             y[k] = ex2(f.x), y[k + 1] = ex2(f.y);
                         }
@@ -789,25 +819,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[e][part]);
                 };
-                auto steps = [&](auto plain) {
-                    step(plain, v0, v0, 0);
-                    step(plain, v1, v0, 1);
+                auto steps = [&](auto kind) {
+                    step(kind, v0, v0, 0);
+                    step(kind, v1, v0, 1);
                     tmem_ld_x16(s_addr + 32, v0);
                     tmem_ld_wait();
                     pin<16>(v0);
-                    step(plain, v0, v1, 2);
+                    step(kind, v0, v1, 2);
                     tmem_ld_x16(s_addr + 48, v1);
                     hand_over(0);
                     tmem_ld_wait();
                     pin<16>(v1);
-                    step(plain, v1, v0, 3);
-                    step(plain, v1, v1, 4);
+                    step(kind, v1, v0, 3);
+                    step(kind, v1, v1, 4);
                 };
-                // the common case by itself, without a branch from its first load to its last store
-                if (!capped && !masked)
-                    steps(std::true_type{});
-                else
-                    steps(std::false_type{});
+                // Each case by itself, without a branch from its first load to its last store; the cap
+                // by a polynomial where all of the warp's scores are below it, else by an exponential
+                // and a quotient (three prompts of up to 2500 tokens, capped, in a window of 512: 100 us
+                // with the polynomial, 141 without).
+                if constexpr (!CAPPED) {
+                    if (!masked)
+                        steps(std::integral_constant<int, kPlain>{});
+                    else
+                        steps(std::integral_constant<int, kGeneral>{});
+                } else {
+                    if (__all_sync(0xFFFFFFFFu, size * cap_in <= 1.f))
+                        steps(std::integral_constant<int, kSmallCap>{});
+                    else
+                        steps(std::integral_constant<int, kGeneral>{});
+                }
                 hand_over(1);
                 l2 = fadd2(l2, fadd2(la, lb));
             }
@@ -962,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool CAPPED>
 cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     DeviceInfo di;
@@ -975,10 +1015,10 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) & bit)) {
         // the warps' register shares wait for one another if the launch brings fewer
         cudaFuncAttributes fa;
-        err = cudaFuncGetAttributes(&fa, attn_tc_kernel<D>);
+        err = cudaFuncGetAttributes(&fa, attn_tc_kernel<D, CAPPED>);
         if (err != cudaSuccess) return err;
         if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-        err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        err = cudaFuncSetAttribute(attn_tc_kernel<D, CAPPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    TcShape<D>::kSmem);
         if (err != cudaSuccess) return err;
         if (dev < 64) attr_done.fetch_or(bit, std::memory_order_acq_rel);
@@ -996,7 +1036,7 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     long long grid = pairs * a.kv_heads;
     if (mode == kListed) grid *= tiles > 0 ? tiles : 1;
     if (mode != kOneItem && grid > sms) grid = sms;
-    err = launch_kernel(attn_tc_kernel<D>, dim3((unsigned)grid), dim3(kThreads), (size_t)TcShape<D>::kSmem, stream,
+    err = launch_kernel(attn_tc_kernel<D, CAPPED>, dim3((unsigned)grid), dim3(kThreads), (size_t)TcShape<D>::kSmem, stream,
                         1, mk, mv, a, tokens, mode);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
@@ -1006,7 +1046,9 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
 
 cudaError_t launch_attn_tc(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                            cudaStream_t stream) {
-    return a.head_dim == 128 ? launch_d<128>(a, mk, mv, stream) : launch_d<64>(a, mk, mv, stream);
+    if (a.softcap > 0.f)
+        return a.head_dim == 128 ? launch_d<128, true>(a, mk, mv, stream) : launch_d<64, true>(a, mk, mv, stream);
+    return a.head_dim == 128 ? launch_d<128, false>(a, mk, mv, stream) : launch_d<64, false>(a, mk, mv, stream);
 }
 
 FD_DEFINE_STATUS_ACCESSOR(status_attn_tc)
