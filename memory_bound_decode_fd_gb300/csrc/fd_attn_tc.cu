@@ -61,7 +61,7 @@ struct TcShape {
     static constexpr int kHalves = D / 64;
     static constexpr int kQ = kTile * D * 2;       // bytes of one half's queries
     static constexpr int kStage = kTile * D * 2;   // a tile of keys or of values
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = 4;
     static constexpr int kSmem = 1024 + 2 * kQ + kStages * kStage;
     // tensor memory columns: S (and P in its first half) and O of both halves
     static constexpr uint32_t kS0 = 0, kO0 = 2 * kTile;
