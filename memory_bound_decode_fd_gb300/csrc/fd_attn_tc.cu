@@ -41,8 +41,8 @@ namespace {
 constexpr int kTile = 128;           // keys of a tile, rows of a half
 constexpr int kSoftmax = 512;        // softmax threads: two for each row, half of its columns each
 constexpr int kHalf = kSoftmax / 2;  // of one half
-constexpr int kMmaWarp = 16, kCopyWarp = 17;
-constexpr int kThreads = 640;        // the last four warps: MMA, copies, two idle
+constexpr int kMmaWarp = 16, kCopyWarp = 17, kDealWarp = 18;
+constexpr int kThreads = 640;        // the last four warps: MMA, copies, dealing, one idle
 // Registers: 640 threads launch with 96 each (61440 in all); 512 x 104 + 128 x 64 = 61440.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
 static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * kLaunchRegs, "registers");
@@ -139,7 +139,6 @@ struct Deal {
     int begin, end;   // of the list, or rounds of whole items
     int run;          // 0: whole items; else the list is dealt out in runs of this length
     int n_pairs;
-    int b, t, hk;     // the one item of a CTA without a list
 };
 
 // One run of tiles of one item (pair of halves, key head).
@@ -152,6 +151,7 @@ struct Segment {
     int lo, hi;        // keys that some row of the pair sees
     int first, last;   // CTAs that share the item
     int next;          // what comes behind the run
+    int valid;         // 0: there are no more runs
 };
 
 __device__ __forceinline__ void clip_halves(Segment &g, const AttnArgs &a, int tokens, int from, int to) {
@@ -180,11 +180,12 @@ __device__ __forceinline__ TileRange pair_tiles(const SeqInfo &s, const AttnArgs
 // The k-th whole item of CTA c: there and back again.
 __device__ __forceinline__ int item_of(int k, int c, int G) { return k * G + (k & 1 ? G - 1 - c : c); }
 
-// What the softmax warps of a half need at the end of a run.
-struct RunEnd {
+// A part of an item that others have the rest of.
+struct Part {
     long long row0;  // activation row of the pair's first token
-    int next, rows, hk, first, last;
+    int rows, hk, first, last;
 };
+constexpr int kRuns = 4;  // runs known ahead
 
 // Barrier over `threads` threads that also tells all of them whether `any` held in one.
 __device__ __forceinline__ bool bar_or(int id, int threads, bool any) {
@@ -211,11 +212,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages], done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, last_s[2];
-    __shared__ Deal deal;
     __shared__ unsigned scan_s[kThreads / 32];
     __shared__ unsigned prefix[kMaxListed + 1];       // tiles of one key head before each pair
     __shared__ unsigned pairs_before[kMaxListed];     // of each sequence
-    __shared__ RunEnd run_end[2][2], joins[2];
+    __shared__ Segment runs[kRuns];
+    __shared__ __align__(8) uint64_t run_full[kRuns], run_empty[kRuns];
+    __shared__ Part joins[2];
+    __shared__ int pick_b, pick_t;                    // the one item of a CTA without a list
     unsigned char *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     const uint32_t q_base = smem_u32(smem), ring = q_base + 2 * T::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -235,8 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&empty[i], 1);
         }
         mbar_init(&done, 1);
+        for (int i = 0; i < kRuns; ++i) {
+            mbar_init(&run_full[i], 1);
+            mbar_init(&run_empty[i], kMmaWarp + 2);  // every warp that works on it
+        }
         abort_flag = 0;
-        deal.begin = deal.end = 0;
+        pick_b = -1;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -246,35 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dep_wait();
     grid_dep_launch();
 
-    // ---------------------------------------------------------------- what this CTA does
     auto pairs_of = [&](int b) { return (unsigned)((load_seq(a.m, b).rows + 2 * tokens - 1) / (2 * tokens)); };
-    // the sequence of pair p
-    auto seq_of = [&](unsigned p) {
-        int b = 0;
-        for (int up = a.m.batch - 1; b < up;) {  // the last one with no more than p pairs before it
-            const int mid = (b + up + 1) >> 1;
-            if (pairs_before[mid] <= p)
-                b = mid;
-            else
-                up = mid - 1;
-        }
-        return b;
-    };
-    const int G = gridDim.x;
-    // What this CTA gets, the largest share of whole items being `most`.
-    auto deal_out = [&](unsigned n_pairs, unsigned all, unsigned most) {
-        const long long total = (long long)all * a.kv_heads;
-        const int n_items = (int)n_pairs * a.kv_heads, c = blockIdx.x;
-        deal.run = 0, deal.n_pairs = (int)n_pairs;
-        if (mode == kPersistent || total >= (1ll << 31) || (long long)most * G <= total + (long long)kJoinTiles * G) {
-            deal.end = n_items / G;
-            if (deal.end * G < n_items && item_of(deal.end, c, G) < n_items) ++deal.end;
-        } else {
-            deal.run = (int)((total + G - 1) / G);
-            const long long begin = (long long)deal.run * c;
-            if (begin < total) deal.begin = (int)begin, deal.end = (int)min(total, begin + deal.run);
-        }
-    };
     if (mode == kOneItem) {
         // the last pairs of a sequence see the most keys, so they come first
         const int per = (a.m.batch + kThreads - 1) / kThreads;
@@ -294,132 +273,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned left = want - at;
             int b = b0;
             for (unsigned n; left >= (n = pairs_of(b)); ++b) left -= n;
-            deal.b = b, deal.t = (int)left, deal.hk = blockIdx.x % a.kv_heads;
-            deal.end = 1;
-        }
-    } else if (warp == 0) {
-        // few sequences: one warp makes the list (a barrier costs more than its other lanes bring)
-        constexpr int kEach = (kMaxListed + 31) / 32;
-        unsigned n[kEach], mine = 0;
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int b = lane * kEach + k;
-            n[k] = b < a.m.batch ? pairs_of(b) : 0;
-            mine += n[k];
-        }
-        const unsigned upto = warp_sum_to(mine, lane);
-        unsigned n_pairs = __shfl_sync(0xFFFFFFFFu, upto, 31), at = upto - mine;
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int b = lane * kEach + k;
-            if (b < a.m.batch) pairs_before[b] = at;
-            at += n[k];
-        }
-        __syncwarp();
-        if (mode == kListed) {
-            n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
-            // one list: key head by key head, pair by pair, tile by tile
-            unsigned most = 0;
-            mine = 0;
-#pragma unroll 1
-            for (int k = 0; k < kEach; ++k) {
-                const unsigned p = lane * kEach + k;
-                unsigned cost = 0;
-                if (p < n_pairs) {
-                    const int b = seq_of(p);
-                    const TileRange r = pair_tiles(load_seq(a.m, b), a, (p - pairs_before[b]) * 2 * tokens, tokens);
-                    cost = r.b - r.a + kItemTiles;
-                    prefix[p] = mine;
-                }
-                mine += cost;
-                most = max(most, cost);
-            }
-            const unsigned sum = warp_sum_to(mine, lane);
-            for (int k = 0; k < kEach; ++k)
-                if (lane * kEach + k < n_pairs) prefix[lane * kEach + k] += sum - mine;
-            const unsigned all = __shfl_sync(0xFFFFFFFFu, sum, 31);
-            most = __reduce_max_sync(0xFFFFFFFFu, most);
-            if (lane == 0) {
-                prefix[n_pairs] = all;
-                deal_out(n_pairs, all, most);
-            }
-        } else if (lane == 0) {
-            deal_out(n_pairs, 0, 0);
+            pick_b = b, pick_t = (int)left;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    if (mode == kListed && deal.n_pairs * a.kv_heads > G) {
-        // Several items a CTA: whole items, the last pairs of a sequence (which see the most keys)
-        // first and the order of the CTAs turned round every time; or, where the longest share of
-        // that is too long, equal runs of the list, joined where they meet.
-        const int n_pairs = deal.n_pairs, n_items = n_pairs * a.kv_heads;
-        unsigned most = 0;
-        if (tid < G) {
-            for (int k = 0; k * G < n_items; ++k) {
-                const int i = item_of(k, tid, G);
-                if (i < n_items) {
-                    const int p = n_pairs - 1 - i / a.kv_heads;
-                    most += prefix[p + 1] - prefix[p];
-                }
-            }
-        }
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        if (lane == 0) scan_s[warp] = most;
-        __syncthreads();
-        if (tid == 0) {
-            for (int w = 0; w < kThreads / 32; ++w) most = max(most, scan_s[w]);
-            deal.begin = deal.end = 0;
-            deal_out(n_pairs, prefix[n_pairs], most);
-        }
-        __syncthreads();
-    }
 
-    auto segment = [&](int x) {
-        Segment g;
-        if (mode == kOneItem || deal.run == 0) {
-            int t;
-            if (mode == kOneItem) {
-                g.b = deal.b, g.hk = deal.hk, t = deal.t;
-            } else {
-                const int i = item_of(x, blockIdx.x, G), p = i / a.kv_heads;
-                const unsigned pair = deal.n_pairs - 1 - p;
-                g.hk = i - p * a.kv_heads, g.b = seq_of(pair), t = (int)(pair - pairs_before[g.b]);
-            }
-            g.s = load_seq(a.m, g.b);
-            g.i0 = t * 2 * tokens;
-            clip_halves(g, a, tokens, 0, 1 << 30);
-            g.first = g.last = 0;
-            g.next = x + 1;
-            return g;
+    // The n-th run, as the dealing warp has written it down (its own waits are the shorter ones, so
+    // this one ends), and that this warp is done with it.
+    auto take = [&](int n) -> const volatile Segment & {
+        const long long t0 = clock64();
+        while (!mbar_try_parity(&run_full[n % kRuns], (uint32_t)(n / kRuns) & 1u) &&
+               clock64() - t0 < 8 * kWaitLimitCycles) {
         }
-        const int head = prefix[deal.n_pairs];
-        g.hk = x / head;
-        const unsigned in_head = (unsigned)(x - g.hk * head);
-        int p = 0;
-        for (int up = deal.n_pairs - 1; p < up;) {  // the last pair with prefix[p] <= in_head
-            const int mid = (p + up + 1) >> 1;
-            if (prefix[mid] <= in_head)
-                p = mid;
-            else
-                up = mid - 1;
-        }
-        g.b = seq_of(p);
-        g.s = load_seq(a.m, g.b);
-        g.i0 = (int)(p - pairs_before[g.b]) * 2 * tokens;
-        const int item0 = g.hk * head + prefix[p], item1 = g.hk * head + prefix[p + 1];
-        const TileRange r = pair_tiles(g.s, a, g.i0, tokens);
-        g.next = min(item1, deal.end);
-        // the run's share of the item's tiles: of v steps, kItemTiles in each (item1 - item0) are
-        // what beginning the item costs
-        const int cost = item1 - item0;
-        auto share = [&](int v) { return v - (kItemTiles * v + cost - 1) / cost; };
-        clip_halves(g, a, tokens, r.a + share(x - item0), r.a + share(g.next - item0));
-        g.first = item0 / deal.run;
-        g.last = (item1 - 1) / deal.run;
-        return g;
+        return runs[n % kRuns];
+    };
+    auto release = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&run_empty[n % kRuns]);
     };
 
     if (warp >= kMmaWarp) {
@@ -435,14 +308,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0, issued = 0;
         bool ok = true;
-        for (int x = deal.begin; x < deal.end && ok;) {
-            const Segment g = segment(x);
-            x = g.next;
+        for (int n = 0;; ++n) {
+            const volatile Segment &g = take(n);
+            if (!g.valid) break;
+            const int hk = g.hk, ja = g.ja, jb = g.jb, lo = g.lo, hi = g.hi;
+            const int *const row = a.m.table + (long long)g.b * a.m.table_stride;
+            release(n);
+            if (!ok) continue;
             auto page_of = [&](int j) {
                 const int tok = j * kTile + my_box * box;
                 int page = a.m.num_pages;  // reads as zeros
-                if (j < g.jb && lane < ops && tok < g.hi && tok + box > g.lo) {
-                    const int id = a.m.table[(long long)g.b * a.m.table_stride + (tok >> a.m.page_shift)];
+                if (j < jb && lane < ops && tok < hi && tok + box > lo) {
+                    const int id = row[tok >> a.m.page_shift];
                     if (id >= 0 && id < a.m.num_pages)
                         page = id;
                     else
@@ -450,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return page;
             };
-            int next_page = page_of(g.ja);
-            for (int j = g.ja; j < g.jb && ok; ++j) {
+            int next_page = page_of(ja);
+            for (int j = ja; j < jb && ok; ++j) {
                 const int page = next_page;
                 next_page = page_of(j + 1);
                 const int off = (j * kTile + my_box * box) & ((1 << a.m.page_shift) - 1);
@@ -463,9 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane < ops) {
                         const MapOrder ord = v ? a.ov : a.ok;
-                        const int y1 = ord.tok == 1 ? off : ord.head == 1 ? g.hk : page;
-                        const int y2 = ord.tok == 2 ? off : ord.head == 2 ? g.hk : page;
-                        const int y3 = ord.tok == 3 ? off : ord.head == 3 ? g.hk : page;
+                        const int y1 = ord.tok == 1 ? off : ord.head == 1 ? hk : page;
+                        const int y2 = ord.tok == 2 ? off : ord.head == 2 ? hk : page;
+                        const int y3 = ord.tok == 3 ? off : ord.head == 3 ? hk : page;
                         tma_load_4d(smem + 2 * T::kQ + stage * T::kStage + dst0, v ? &map_v : &map_k, my_half * 64,
                                     y1, y2, y3, &full[stage], policy);
                     }
@@ -513,13 +390,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) tc_commit(bar);
             __syncwarp();
         };
-        for (int x = deal.begin; x < deal.end && ok;) {
-            const Segment g = segment(x);
-            x = g.next;
+        for (int n = 0;; ++n) {
+            const volatile Segment &g = take(n);
+            if (!same(g.valid)) break;
             const int ja = same(g.ja), jb = same(g.jb), lo = same(g.lo), hi = same(g.hi);
             const int ha[2] = {(int)same(g.h[0].a), (int)same(g.h[1].a)}, hb[2] = {(int)same(g.h[0].b), (int)same(g.h[1].b)};
+            release(n);
+            if (!ok) continue;
             if (jb <= ja) continue;
-            if (!wait(&full[stage], phase)) break;
+            if (!wait(&full[stage], phase)) continue;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (hb[e] > ha[e]) {
@@ -528,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     if (ja >= ha[e]) scores(e, stage);
                 }
-            if (!ok) break;
+            if (!ok) continue;
             commit(&empty[stage]);
             if (++stage == T::kStages) stage = 0, phase ^= 1u;
             for (int j = ja; j < jb && ok; ++j) {
@@ -595,6 +474,148 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_hw(&done, 0);
         }
         __syncwarp();
+    } else if (warp == kDealWarp) {
+        // ----------------------------------------------------- what this CTA does, run by run
+        const int G = gridDim.x, c = blockIdx.x;
+        // the sequence of pair p
+        auto seq_of = [&](unsigned p) {
+            int b = 0;
+            for (int up = a.m.batch - 1; b < up;) {  // the last one with no more than p pairs before it
+                const int mid = (b + up + 1) >> 1;
+                if (pairs_before[mid] <= p)
+                    b = mid;
+                else
+                    up = mid - 1;
+            }
+            return b;
+        };
+        Deal deal{0, 0, 0, 0};
+        if (mode == kOneItem) {
+            deal.end = pick_b >= 0;
+        } else {
+            constexpr int kEach = (kMaxListed + 31) / 32;
+            unsigned mine = 0;
+#pragma unroll 1
+            for (int k = 0; k < kEach; ++k) {
+                const int b = lane * kEach + k;
+                if (b < a.m.batch) {
+                    pairs_before[b] = mine;  // of this lane's sequences
+                    mine += pairs_of(b);
+                }
+            }
+            const unsigned upto = warp_sum_to(mine, lane);
+            unsigned n_pairs = __shfl_sync(0xFFFFFFFFu, upto, 31);
+            for (int k = 0; k < kEach; ++k)
+                if (lane * kEach + k < a.m.batch) pairs_before[lane * kEach + k] += upto - mine;
+            __syncwarp();
+            unsigned all = 0, most = 0;  // the list's length for one key head; the largest share of whole items
+            if (mode == kListed) {
+                n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
+                // one list: key head by key head, pair by pair, tile by tile
+                mine = 0;
+#pragma unroll 1
+                for (int k = 0; k < kEach; ++k) {
+                    const unsigned p = lane * kEach + k;
+                    if (p < n_pairs) {
+                        const int b = seq_of(p);
+                        const TileRange r = pair_tiles(load_seq(a.m, b), a, (p - pairs_before[b]) * 2 * tokens, tokens);
+                        const unsigned cost = r.b - r.a + kItemTiles;
+                        prefix[p] = mine;
+                        mine += cost;
+                        most = max(most, cost);
+                    }
+                }
+                const unsigned sum = warp_sum_to(mine, lane);
+                for (int k = 0; k < kEach; ++k)
+                    if (lane * kEach + k < n_pairs) prefix[lane * kEach + k] += sum - mine;
+                all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+                if (lane == 0) prefix[n_pairs] = all;
+                __syncwarp();
+            }
+            // Whole items, the last pairs of a sequence (which see the most keys) first and the order of
+            // the CTAs turned round every time; or, where the longest share of that is too long, equal
+            // runs of the list, joined where they meet.
+            const int n_items = (int)n_pairs * a.kv_heads;
+            if (mode == kListed && n_items > G) {
+                most = 0;
+                for (int cta = lane; cta < G; cta += 32) {
+                    unsigned share = 0;
+                    for (int k = 0; k * G < n_items; ++k) {
+                        const int i = item_of(k, cta, G);
+                        if (i < n_items) {
+                            const int p = (int)n_pairs - 1 - i / a.kv_heads;
+                            share += prefix[p + 1] - prefix[p];
+                        }
+                    }
+                    most = max(most, share);
+                }
+            }
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            const long long total = (long long)all * a.kv_heads;
+            deal.n_pairs = (int)n_pairs;
+            if (mode == kPersistent || total >= (1ll << 31) || (long long)most * G <= total + (long long)kJoinTiles * G) {
+                deal.end = n_items / G;
+                if (deal.end * G < n_items && item_of(deal.end, c, G) < n_items) ++deal.end;
+            } else {
+                deal.run = (int)((total + G - 1) / G);
+                const long long begin = (long long)deal.run * c;
+                if (begin < total) deal.begin = (int)begin, deal.end = (int)min(total, begin + deal.run);
+            }
+        }
+        int x = deal.begin;
+        for (int n = 0;; ++n) {
+            Segment g{};
+            if (x < deal.end) {
+                g.valid = 1;
+                int from = 0, to = 1 << 30, t;
+                g.next = x + 1;
+                if (mode == kOneItem) {
+                    g.b = pick_b, g.hk = c % a.kv_heads, t = pick_t;
+                } else if (deal.run == 0) {
+                    const int i = item_of(x, c, G), p = i / a.kv_heads;
+                    const unsigned pair = deal.n_pairs - 1 - p;
+                    g.hk = i - p * a.kv_heads, g.b = seq_of(pair), t = (int)(pair - pairs_before[g.b]);
+                } else {
+                    const int head = prefix[deal.n_pairs];
+                    g.hk = x / head;
+                    const unsigned in_head = (unsigned)(x - g.hk * head);
+                    int p = 0;
+                    for (int up = deal.n_pairs - 1; p < up;) {  // the last pair with prefix[p] <= in_head
+                        const int mid = (p + up + 1) >> 1;
+                        if (prefix[mid] <= in_head)
+                            p = mid;
+                        else
+                            up = mid - 1;
+                    }
+                    g.b = seq_of(p), t = (int)(p - pairs_before[g.b]);
+                    const int item0 = g.hk * head + prefix[p], item1 = g.hk * head + prefix[p + 1];
+                    g.next = min(item1, deal.end);
+                    // the run's share of the item's tiles: of v steps, kItemTiles in each
+                    // (item1 - item0) are what beginning the item costs
+                    const int cost = item1 - item0;
+                    auto share = [&](int v) { return v - (kItemTiles * v + cost - 1) / cost; };
+                    from = share(x - item0), to = share(g.next - item0);
+                    g.first = item0 / deal.run;
+                    g.last = (item1 - 1) / deal.run;
+                }
+                g.s = load_seq(a.m, g.b);
+                g.i0 = t * 2 * tokens;
+                const int base = deal.run == 0 ? 0 : pair_tiles(g.s, a, g.i0, tokens).a;
+                clip_halves(g, a, tokens, base + from, base + to);
+                x = g.next;
+            }
+            // room for it (bounded: those who hold a run give up on their own waits)
+            const long long t0 = clock64();
+            while (!mbar_try_parity(&run_empty[n % kRuns], ((uint32_t)(n / kRuns) & 1u) ^ 1u) &&
+                   clock64() - t0 < 4 * kWaitLimitCycles) {
+            }
+            if (lane == 0) {
+                runs[n % kRuns] = g;
+                mbar_arrive(&run_full[n % kRuns]);
+            }
+            __syncwarp();
+            if (!g.valid) break;
+        }
     }
     } else {
         // ----------------------------------------------------------------- softmax
@@ -620,32 +641,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_ph = 0, o_ph = 0;
         bool dead = false;
         constexpr int kSlot = tc_slot_words(D);
-        // What the end of a run needs is kept in shared memory: registers are short in its loop.
-        volatile RunEnd *const ends = run_end[e];
         int ja = 0, jb = 0, lo = 0, hi = 0, in_lo = 0, in_hi = 0;
         constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;  // of a row of Q in 16-byte loads
         constexpr int kLoads = 16 / kRowsAtOnce;                  // 16 rows a warp
         uint4 q_next[kLoads];
-        // Takes up the run at x: its tiles and visible keys for this row, and 16 rows of Q.
-        auto enter = [&](int x, int which) {
-            const Segment g = segment(x);
-            const int i_first = g.i0 + e * tokens, i_last = min(g.s.rows, i_first + tokens) - 1;
+        // Takes up the n-th run: its tiles and visible keys for this row, and 16 rows of Q. False: there
+        // is none.
+        auto enter = [&](int n) {
+            const volatile Segment &g = take(n);
+            if (!g.valid) return false;
+            const SeqInfo seq{g.s.q0, g.s.rows, g.s.kv, g.s.base};
+            const int i_first = g.i0 + e * tokens, i_last = min(seq.rows, i_first + tokens) - 1, head0 = g.hk * a.group;
             const int tl = r / a.group, i = i_first + tl;
-            const bool live = tl < tokens && i < g.s.rows;
+            const bool live = tl < tokens && i < seq.rows;
             ja = e ? g.h[1].a : g.h[0].a, jb = e ? g.h[1].b : g.h[0].b;
-            hi = live ? key_hi(g.s, i, a.causal) : 0, lo = live ? key_lo(g.s, i, a.window) : 0;
-            in_hi = key_hi(g.s, i_first, a.causal), in_lo = key_lo(g.s, i_last, a.window);
-            if (tid == e * kHalf) {
-                volatile RunEnd &t = ends[which];
-                t.next = g.next, t.row0 = g.s.q0 + g.i0, t.rows = g.s.rows - g.i0, t.hk = g.hk;
-                t.first = g.first, t.last = g.last;
-            }
+            hi = live ? key_hi(seq, i, a.causal) : 0, lo = live ? key_lo(seq, i, a.window) : 0;
+            in_hi = key_hi(seq, i_first, a.causal), in_lo = key_lo(seq, i_last, a.window);
             if (jb > ja) {
                 // whole rows in a load: lane l knows where row (l & 15) of the warp's 16 begins
                 const int row = (warp & 7) * 16 + (lane & 15), t = row / a.group;
-                const bool there = t < tokens && i_first + t < g.s.rows;
-                const long long at = there ? (long long)(g.s.q0 + i_first + t) * a.q.ts +
-                                                 (g.hk * a.group + row - t * a.group) * a.q.hs : 0;
+                const bool there = t < tokens && i_first + t < seq.rows;
+                const long long at = there ? (long long)(seq.q0 + i_first + t) * a.q.ts +
+                                                 (head0 + row - t * a.group) * a.q.hs : 0;
                 const uint32_t rows = __ballot_sync(0xFFFFFFFFu, there);
 #pragma unroll
                 for (int n = 0; n < kLoads; ++n) {
@@ -655,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ? *reinterpret_cast<const uint4 *>(a.q.p + from + lane % kLanes * 8) : make_uint4(0, 0, 0, 0);
                 }
             }
+            return true;
         };
         // The rows into the swizzled tile (rows without a token: zeros).
         auto put_q = [&]() {
@@ -670,14 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[e]);
         };
-        bool more = deal.begin < deal.end;
-        int run = 0, n_joins = 0;
-        if (more) {
-            enter(deal.begin, 0);
-            if (jb > ja) put_q();
-        }
-        for (; more; run ^= 1) {
-            named_bar_sync(bar, kHalf);  // ends[run] is written, ends[run ^ 1] no longer read
+        int n_joins = 0;
+        bool more = enter(0);
+        if (more && jb > ja) put_q();
+        for (int run = 0; more; ++run) {
             float m = -INFINITY;  // what the exponentials are taken against, log2 units
             float2 l2 = make_float2(0.f, 0.f);
             const bool any = jb > ja && !dead;
@@ -854,8 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------- the run's result
             // The next run's queries are read while the last MMAs end, and given to the MMA warp
             // before this run's result is written.
-            more = ends[run].next < deal.end;
-            if (more) enter(ends[run].next, run ^ 1);
+            more = enter(run + 1);
             float l = l2.x + l2.y;
             if (any) {
                 // the other half of the row's sum, by way of the scores' first columns, now free
@@ -879,10 +892,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m2 = m;
             if (dead) l = NAN, m2 = 0.f;
             const int tl = r / a.group;
-            const int first = ends[run].first, last = ends[run].last, n_tokens = ends[run].rows;
+            const volatile Segment &g = runs[run % kRuns];
+            const int first = g.first, last = g.last, n_tokens = g.s.rows - g.i0;
             const bool whole = first == last, live = tl < tokens && e * tokens + tl < n_tokens;
-            const int h = ends[run].hk * a.group + r - tl * a.group;
-            const long long tok0 = ends[run].row0, tok = tok0 + e * tokens + tl;
+            const int hk = g.hk, h = hk * a.group + r - tl * a.group;
+            const long long tok0 = g.s.q0 + g.i0, tok = tok0 + e * tokens + tl;
+            release(run);
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
             // whole: a row of the result; else of this CTA's slot, [D / 4][256 rows] of 4 floats, then
             // (maximum, sum) of each row
@@ -926,8 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.lse[tok * a.q_heads + h] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
             }
             if (!whole && tid == 0) {  // joined below
-                RunEnd &t = joins[n_joins];
-                t.row0 = tok0, t.rows = n_tokens, t.hk = ends[run].hk, t.first = first, t.last = last;
+                joins[n_joins] = Part{tok0, n_tokens, hk, first, last};
             }
             n_joins += !whole;
             tc_fence_before();  // the loads of O, before the next run's MMAs
