@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
         constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D) | (1u << 16);  // B is N-major
         // What the tensor-core instructions take is kept the same in all lanes, and broadcast, so
-        // that it lies in uniform registers: issued from others, one MMA took 110 cycles.
+        // that it lies in uniform registers: issued from others, one MMA took 110 cycles. Broadcast
+        // where it is used, or all of the loop's descriptors are kept in registers, and spill.
         auto same = [](uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
         const uint32_t tm = same(tmem), q_desc = same(desc_sw128_low(q_base)), k_desc = same(desc_sw128_low(ring));
         const uint32_t v_desc = same(desc_sw128_mn_low(ring, kTile * 128));
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return ok;
         };
         auto scores = [&](int e, int st) {  // S_e = Q_e K^T
-            const uint32_t qd = q_desc + e * (T::kQ >> 4), kd = k_desc + st * (T::kStage >> 4);
+            const uint32_t qd = same(q_desc + e * (T::kQ >> 4)), kd = same(k_desc + st * (T::kStage >> 4));
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                const uint32_t vd = v_desc + vs * (T::kStage >> 4);
+                const uint32_t vd = same(v_desc + vs * (T::kStage >> 4));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (j >= ha[e] && j < hb[e]) {
