@@ -494,42 +494,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mode == kOneItem) {
             deal.end = pick_b >= 0;
         } else {
-            constexpr int kEach = (kMaxListed + 31) / 32;
-            unsigned mine = 0;
+            unsigned n_pairs = 0;
 #pragma unroll 1
-            for (int k = 0; k < kEach; ++k) {
-                const int b = lane * kEach + k;
-                if (b < a.m.batch) {
-                    pairs_before[b] = mine;  // of this lane's sequences
-                    mine += pairs_of(b);
-                }
+            for (int b0 = 0; b0 < a.m.batch; b0 += 32) {
+                const int b = b0 + lane;
+                const unsigned n = b < a.m.batch ? pairs_of(b) : 0, upto = warp_sum_to(n, lane);
+                if (b < a.m.batch) pairs_before[b] = n_pairs + upto - n;
+                n_pairs += __shfl_sync(0xFFFFFFFFu, upto, 31);
             }
-            const unsigned upto = warp_sum_to(mine, lane);
-            unsigned n_pairs = __shfl_sync(0xFFFFFFFFu, upto, 31);
-            for (int k = 0; k < kEach; ++k)
-                if (lane * kEach + k < a.m.batch) pairs_before[lane * kEach + k] += upto - mine;
             __syncwarp();
             unsigned all = 0, most = 0;  // the list's length for one key head; the largest share of whole items
             if (mode == kListed) {
                 n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
                 // one list: key head by key head, pair by pair, tile by tile
-                mine = 0;
 #pragma unroll 1
-                for (int k = 0; k < kEach; ++k) {
-                    const unsigned p = lane * kEach + k;
+                for (unsigned p0 = 0; p0 < n_pairs; p0 += 32) {
+                    const unsigned p = p0 + lane;
+                    unsigned cost = 0;
                     if (p < n_pairs) {
                         const int b = seq_of(p);
                         const TileRange r = pair_tiles(load_seq(a.m, b), a, (p - pairs_before[b]) * 2 * tokens, tokens);
-                        const unsigned cost = r.b - r.a + kItemTiles;
-                        prefix[p] = mine;
-                        mine += cost;
-                        most = max(most, cost);
+                        cost = r.b - r.a + kItemTiles;
                     }
+                    const unsigned upto = warp_sum_to(cost, lane);
+                    if (p < n_pairs) prefix[p] = all + upto - cost;
+                    all += __shfl_sync(0xFFFFFFFFu, upto, 31);
+                    most = max(most, cost);
                 }
-                const unsigned sum = warp_sum_to(mine, lane);
-                for (int k = 0; k < kEach; ++k)
-                    if (lane * kEach + k < n_pairs) prefix[lane * kEach + k] += sum - mine;
-                all = __shfl_sync(0xFFFFFFFFu, sum, 31);
                 if (lane == 0) prefix[n_pairs] = all;
                 __syncwarp();
             }
@@ -538,18 +529,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             // runs of the list, joined where they meet.
             const int n_items = (int)n_pairs * a.kv_heads;
             if (mode == kListed && n_items > G) {
-                most = 0;
-                for (int cta = lane; cta < G; cta += 32) {
-                    unsigned share = 0;
-                    for (int k = 0; k * G < n_items; ++k) {
-                        const int i = item_of(k, cta, G);
-                        if (i < n_items) {
-                            const int p = (int)n_pairs - 1 - i / a.kv_heads;
-                            share += prefix[p + 1] - prefix[p];
+                unsigned share[kAttnMaxCtas / 32] = {};
+                const unsigned magic = 0xFFFFFFFFu / (unsigned)a.kv_heads + 1u;  // i / kv_heads, i < 2^18
+#pragma unroll 1
+                for (int k = 0; k * G < n_items; ++k) {
+#pragma unroll
+                    for (int q = 0; q < kAttnMaxCtas / 32; ++q) {
+                        const int cta = lane + 32 * q, i = item_of(k, cta, G);
+                        if (cta < G && i < n_items) {
+                            const int p = (int)n_pairs - 1 -
+                                          (a.kv_heads == 1 ? i : (int)__umulhi((unsigned)i, magic));
+                            share[q] += prefix[p + 1] - prefix[p];
                         }
                     }
-                    most = max(most, share);
                 }
+                most = 0;
+#pragma unroll
+                for (int q = 0; q < kAttnMaxCtas / 32; ++q) most = max(most, share[q]);
             }
             most = __reduce_max_sync(0xFFFFFFFFu, most);
             const long long total = (long long)all * a.kv_heads;
@@ -629,12 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_addr = lane_base + T::kS0 + e * kTile + cg * 64;
         const uint32_t o_addr = lane_base + T::kO0 + e * kTile + cg * (D / 2);
-        // A negative scale is put into Q's signs and a scale of 0 into zeros, so that what follows
-        // is monotone in S: the maximum of a row is taken before scale and cap.
-        const uint32_t q_and = a.scale == 0.f ? 0u : 0xFFFFFFFFu, q_xor = a.scale < 0.f ? 0x80008000u : 0u;
-        const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
-        const float cap_in = CAPPED ? scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
-        const float mul = CAPPED ? cap_in * (2.f * kLog2e) : scale * kLog2e;
+        // The scale is positive (attn_uses_tc), so that what follows is monotone in S: the maximum of a
+        // row is taken before scale and cap.
+        const float cap_in = CAPPED ? a.scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+        const float mul = CAPPED ? cap_in * (2.f * kLog2e) : a.scale * kLog2e;
         // a score in log2 units; c tanh(y) = c (1 - 2 / (e^(2 y) + 1))
         auto log2_score = [&](float v) {
             return CAPPED ? cap_out - __fdividef(2.f * cap_out, ex2(v * mul) + 1.f) : v * mul;
@@ -645,53 +639,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ja = 0, jb = 0, lo = 0, hi = 0, in_lo = 0, in_hi = 0;
         constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;  // of a row of Q in 16-byte loads
         constexpr int kLoads = 16 / kRowsAtOnce;                  // 16 rows a warp
-        uint4 q_next[kLoads];
+        int head0 = 0, row0 = 0, rows = 0;  // of the run's Q: first head and row, tokens of the half
         // Takes up the n-th run: its tiles and visible keys for this row, and 16 rows of Q. False: there
         // is none.
         auto enter = [&](int n) {
             const volatile Segment &g = take(n);
             if (!g.valid) return false;
             const SeqInfo seq{g.s.q0, g.s.rows, g.s.kv, g.s.base};
-            const int i_first = g.i0 + e * tokens, i_last = min(seq.rows, i_first + tokens) - 1, head0 = g.hk * a.group;
+            const int i_first = g.i0 + e * tokens, i_last = min(seq.rows, i_first + tokens) - 1;
             const int tl = r / a.group, i = i_first + tl;
             const bool live = tl < tokens && i < seq.rows;
             ja = e ? g.h[1].a : g.h[0].a, jb = e ? g.h[1].b : g.h[0].b;
             hi = live ? key_hi(seq, i, a.causal) : 0, lo = live ? key_lo(seq, i, a.window) : 0;
             in_hi = key_hi(seq, i_first, a.causal), in_lo = key_lo(seq, i_last, a.window);
-            if (jb > ja) {
-                // whole rows in a load: lane l knows where row (l & 15) of the warp's 16 begins
-                const int row = (warp & 7) * 16 + (lane & 15), t = row / a.group;
-                const bool there = t < tokens && i_first + t < seq.rows;
-                const long long at = there ? (long long)(seq.q0 + i_first + t) * a.q.ts +
-                                                 (head0 + row - t * a.group) * a.q.hs : 0;
-                const uint32_t rows = __ballot_sync(0xFFFFFFFFu, there);
-#pragma unroll
-                for (int n = 0; n < kLoads; ++n) {
-                    const int k = n * kRowsAtOnce + lane / kLanes;
-                    const long long from = __shfl_sync(0xFFFFFFFFu, at, k);
-                    q_next[n] = rows >> k & 1
-                        ? *reinterpret_cast<const uint4 *>(a.q.p + from + lane % kLanes * 8) : make_uint4(0, 0, 0, 0);
-                }
-            }
+            head0 = g.hk * a.group, row0 = seq.q0 + i_first, rows = min(tokens, seq.rows - i_first);
             return true;
         };
-        // The rows into the swizzled tile (rows without a token: zeros).
-        auto put_q = [&]() {
-#pragma unroll
+        // 16 rows of Q into the swizzled tile, asynchronously (rows without a token: zeros), and their
+        // arrival. A loop, not unrolled: this is the first code of a launch, read from far.
+        auto fetch_q = [&]() {
+#pragma unroll 1
             for (int n = 0; n < kLoads; ++n) {
                 const int row = (warp & 7) * 16 + n * kRowsAtOnce + lane / kLanes, c = lane % kLanes;
-                uint4 v = q_next[n];
-                v.x = and_xor(v.x, q_and, q_xor), v.y = and_xor(v.y, q_and, q_xor);
-                v.z = and_xor(v.z, q_and, q_xor), v.w = and_xor(v.w, q_and, q_xor);
-                sts_v4(q_base + e * T::kQ + row * 128 + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4), v);
+                const int t = row / a.group;
+                const uint16_t *from = a.q.p + (long long)(row0 + t) * a.q.ts + (head0 + row - t * a.group) * a.q.hs + c * 8;
+                const bool there = t < rows;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 q_base + e * T::kQ + row * 128 + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4)),
+                             "l"(there ? from : a.q.p), "r"(there ? 16 : 0)
+                             : "memory");
             }
+        };
+        auto give_q = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[e]);
         };
         int n_joins = 0;
         bool more = enter(0);
-        if (more && jb > ja) put_q();
+        if (more && jb > ja) {
+            fetch_q();
+            give_q();
+        }
         for (int run = 0; more; ++run) {
             float m = -INFINITY;  // what the exponentials are taken against, log2 units
             float2 l2 = make_float2(0.f, 0.f);
@@ -867,8 +857,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l2 = fadd2(l2, fadd2(la, lb));
             }
             // ------------------------------------------------------- the run's result
-            // The next run's queries are read while the last MMAs end, and given to the MMA warp
-            // before this run's result is written.
             more = enter(run + 1);
             float l = l2.x + l2.y;
             if (any) {
@@ -889,7 +877,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = cg ? __uint_as_float(other) + l : l + __uint_as_float(other);
                 tc_fence_before();
             }
-            if (more && jb > ja) put_q();
+            const bool next_q = more && jb > ja;  // Q's tile is free: nothing of this run reads it any more
+            if (next_q) fetch_q();
             float m2 = m;
             if (dead) l = NAN, m2 = 0.f;
             const int tl = r / a.group;
@@ -934,6 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
                                            __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])));
                 }
+                if (c == 0 && next_q) give_q();  // read meanwhile; the next scores need not wait for the rest
             }
             if (live && cg == 0) {
                 if (!whole)
