@@ -52,9 +52,11 @@ enum { kOneItem, kListed, kPersistent };
 // How scores become exponents (softmax steps).
 enum { kPlain, kSmallCap, kGeneral };
 constexpr float kRaise = 8.f;        // log2 units
-// What beginning an item costs (its queries loaded, the last result written), and what joining the
-// parts of one costs, in tiles.
-constexpr int kItemTiles = 2, kJoinTiles = 6;
+// In tiles: what beginning an item costs (its queries loaded, the last result written), and what
+// joining the parts of one costs, at all and for each part of 256 rows (128 KB written and read
+// again).
+constexpr int kItemTiles = 2, kJoinTiles = 4;
+constexpr float kPartTiles = 1.2f;
 
 template <int D>
 struct TcShape {
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 n_pairs += __shfl_sync(0xFFFFFFFFu, upto, 31);
             }
             __syncwarp();
-            unsigned all = 0, most = 0;  // the list's length for one key head; the largest share of whole items
+            unsigned all = 0, most = 0;  // the list's length for one key head; the longest item
             if (mode == kListed) {
                 n_pairs = min(n_pairs, (unsigned)kMaxListed);  // more only where sequences share rows
                 // one list: key head by key head, pair by pair, tile by tile
@@ -526,7 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Whole items, the last pairs of a sequence (which see the most keys) first and the order of
             // the CTAs turned round every time; or, where the longest share of that is too long, equal
-            // runs of the list, joined where they meet.
+            // runs of the list, joined where they meet. A run is long enough that joining an item's
+            // parts takes no longer than one: C / run parts of f each cost as much as the run at
+            // run = sqrt(f C).
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            const float part = kPartTiles / 256.f * (float)min((long long)a.m.max_q * a.group, 256ll);
+            const long long total = (long long)all * a.kv_heads;
+            const long long run = max((total + G - 1) / G, (long long)ceilf(sqrtf(part * (float)most)));
+            const float joined = (float)run + kJoinTiles + part * ceilf((float)most / (float)max(run, 1ll));
             const int n_items = (int)n_pairs * a.kv_heads;
             if (mode == kListed && n_items > G) {
                 unsigned share[kAttnMaxCtas / 32] = {};
@@ -547,16 +556,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < kAttnMaxCtas / 32; ++q) most = max(most, share[q]);
             }
-            most = __reduce_max_sync(0xFFFFFFFFu, most);
-            const long long total = (long long)all * a.kv_heads;
+            most = __reduce_max_sync(0xFFFFFFFFu, most);  // of the shares, or of the items where they are that
             deal.n_pairs = (int)n_pairs;
-            if (mode == kPersistent || total >= (1ll << 31) || (long long)most * G <= total + (long long)kJoinTiles * G) {
+            if (mode == kPersistent || total >= (1ll << 31) || (float)most <= joined) {
                 deal.end = n_items / G;
                 if (deal.end * G < n_items && item_of(deal.end, c, G) < n_items) ++deal.end;
             } else {
-                deal.run = (int)((total + G - 1) / G);
-                const long long begin = (long long)deal.run * c;
-                if (begin < total) deal.begin = (int)begin, deal.end = (int)min(total, begin + deal.run);
+                deal.run = (int)run;
+                const long long begin = run * c;
+                if (begin < total) deal.begin = (int)begin, deal.end = (int)min(total, begin + run);
             }
         }
         int x = deal.begin;
