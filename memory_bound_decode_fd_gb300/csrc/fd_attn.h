@@ -69,6 +69,13 @@ struct AttnArgs {
     float softcap;    // 0: none
     unsigned *counters;  // one per CTA, zero between calls
     float *partials;     // one slot for the first and one for the last item of each CTA
+    struct AttnPart *parts;  // of fd_attn_tc.cu: one for each CTA
+};
+// An item that begins in one CTA and ends in another (last < 0: there is none).
+struct AttnPart {
+    long long row0;  // activation row of the first token
+    int rows, hk;    // tokens from there on, key head
+    int first, last; // the CTAs that share it
 };
 
 constexpr int kAttnMaxCtas = 256;             // largest grid (counters in the scratch)

@@ -305,8 +305,9 @@ size_t fd_paged_attention_scratch_bytes(int batch, int total_q, int q_heads, int
         (head_dim != 64 && head_dim != 128))
         return 0;
     const size_t slots = 2 * kAttnMaxCtas * sizeof(float);
-    return kAttnCounterBytes + slots * (attn_uses_tc(max_q, q_heads / kv_heads, 1.f) ? tc_slot_words(head_dim)
-                                                                               : rows_slot_words(head_dim));
+    if (attn_uses_tc(max_q, q_heads / kv_heads, 1.f))
+        return kAttnCounterBytes + slots * tc_slot_words(head_dim) + kAttnMaxCtas * sizeof(AttnPart);
+    return kAttnCounterBytes + slots * rows_slot_words(head_dim);
 }
 
 int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_paged_batch *batch,
@@ -353,6 +354,7 @@ int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_
     a.counters = static_cast<unsigned *>(scratch);
     a.partials = reinterpret_cast<float *>(static_cast<unsigned char *>(scratch) + kAttnCounterBytes);
     const bool tc = attn_uses_tc(a.m.max_q, a.group, scale);
+    if (tc) a.parts = reinterpret_cast<AttnPart *>(a.partials + (size_t)2 * kAttnMaxCtas * tc_slot_words(d));
     const int most = tc ? kAttnTcTile : kRowsBox;
     const int box = cache->page_size < most ? cache->page_size : most;
     CUtensorMap mk, mv;

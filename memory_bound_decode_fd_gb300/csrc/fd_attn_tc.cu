@@ -23,12 +23,13 @@
 //     relative at most), the row's sum is that of the unrounded values, in fp32.
 //   * Work: up to kMaxListed pairs of halves and the grid is one CTA an SM, which deals itself
 //     items (a pair and a key head), or, where whole items do not come out even, equal runs of the
-//     tiles of all items; an item that several CTAs share is joined by the last of them (a
-//     ticket), in CTA order. More pairs, and each CTA takes one item, the longest first.
+//     tiles of all items; what several CTAs share is joined by a second kernel. With more sequences
+//     than a CTA lists, each takes one item, the longest first.
 //   * Values of the first and last tile that no row of the item sees are cleared in shared memory
 //     before their MMA (0 x NaN): pages hold anything past the last token.
 //   * Every wait is bounded; a CTA that gives up writes NaN, drains its copies and MMAs and frees
 //     its tensor memory.
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -56,7 +57,7 @@ constexpr float kRaise = 8.f;        // log2 units
 // joining the parts of one costs, at all and for each part of 256 rows (128 KB written and read
 // again).
 constexpr int kItemTiles = 2, kJoinTiles = 4;
-constexpr float kPartTiles = 1.2f;
+constexpr float kPartTiles = 0.3f;
 
 template <int D>
 struct TcShape {
@@ -182,11 +183,6 @@ __device__ __forceinline__ TileRange pair_tiles(const SeqInfo &s, const AttnArgs
 // The k-th whole item of CTA c: there and back again.
 __device__ __forceinline__ int item_of(int k, int c, int G) { return k * G + (k & 1 ? G - 1 - c : c); }
 
-// A part of an item that others have the rest of.
-struct Part {
-    long long row0;  // activation row of the pair's first token
-    int rows, hk, first, last;
-};
 constexpr int kRuns = 4;  // runs known ahead
 
 // Barrier over `threads` threads that also tells all of them whether `any` held in one.
@@ -213,13 +209,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages], done;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, last_s[2];
+    __shared__ int abort_flag;
     __shared__ unsigned scan_s[kThreads / 32];
     __shared__ unsigned prefix[kMaxListed + 1];       // tiles of one key head before each pair
     __shared__ unsigned pairs_before[kMaxListed];     // of each sequence
     __shared__ Segment runs[kRuns];
     __shared__ __align__(8) uint64_t run_full[kRuns], run_empty[kRuns];
-    __shared__ Part joins[2];
     __shared__ int pick_b, pick_t;                    // the one item of a CTA without a list
     unsigned char *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     const uint32_t q_base = smem_u32(smem), ring = q_base + 2 * T::kQ;
@@ -684,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[e]);
         };
-        int n_joins = 0;
+        AttnPart part{0, 0, 0, 0, -1};
         bool more = enter(0);
         if (more && jb > ja) {
             fetch_q();
@@ -939,73 +934,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else if (a.lse)
                     a.lse[tok * a.q_heads + h] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
             }
-            if (!whole && tid == 0) {  // joined below
-                joins[n_joins] = Part{tok0, n_tokens, hk, first, last};
-            }
-            n_joins += !whole;
+            if (tid == 0 && !whole && (int)blockIdx.x == first) part = AttnPart{tok0, n_tokens, hk, first, last};
             tc_fence_before();  // the loads of O, before the next run's MMAs
         }
-        // ----------------------------------------- items that this CTA shares with others
-        if (n_joins > 0) {
-            __threadfence();
-            named_bar_sync(1, kSoftmax);
-            if (tid < n_joins) {
-                const int first = joins[tid].first;
-                const unsigned ticket = atomicAdd(&a.counters[first], 1u);
-                last_s[tid] = ticket == (unsigned)(joins[tid].last - first);
-                if (last_s[tid]) a.counters[first] = 0;
-                __threadfence();
-            }
-            named_bar_sync(1, kSoftmax);
-        }
-        for (int n = 0; n < n_joins; ++n) {
-            if (!last_s[n]) continue;
-            const int first = joins[n].first, last = joins[n].last;
-            // rows (token, head) of the pair that exist, 32 elements of one at a time: 8 loads of each
-            // part in flight
-            const int n_rows0 = min(tokens, joins[n].rows) * a.group;
-            const int n_rows = n_rows0 + max(0, min(tokens, joins[n].rows - tokens)) * a.group;
-            for (int idx = tid; idx < n_rows * (D / 32); idx += kSoftmax) {
-                const int d0 = idx / n_rows * 8;
-                int rr = idx % n_rows;
-                const int he = rr >= n_rows0;
-                if (he) rr -= n_rows0;
-                const int at_row = he * kTile + rr;
-                auto slot_of = [&](int k) {
-                    return a.partials + (size_t)(2 * k + (k == first ? 1 : 0)) * kSlot;
-                };
-                float M = -INFINITY, L = 0.f;
-#pragma unroll 4
-                for (int k = first; k <= last; ++k) M = fmaxf(M, __ldcg(slot_of(k) + 2 * kTile * D + 2 * at_row));
-                const float base = M == -INFINITY ? 0.f : M;
-                float4 acc[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k = first; k <= last; ++k) {
-                    const float *sl = slot_of(k);
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kTile * D) + at_row);
-                    const float f = ex2(ml.x - base);
-                    L = fmaf(ml.y, f, L);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(sl) + (d0 + q) * (2 * kTile) + at_row);
-                        acc[q].x = fmaf(v.x, f, acc[q].x), acc[q].y = fmaf(v.y, f, acc[q].y);
-                        acc[q].z = fmaf(v.z, f, acc[q].z), acc[q].w = fmaf(v.w, f, acc[q].w);
-                    }
-                }
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-                const int tt = rr / a.group, hh = joins[n].hk * a.group + rr - tt * a.group;
-                const long long to = joins[n].row0 + he * tokens + tt;
-                uint16_t *out = a.out.p + to * a.out.ts + hh * a.out.hs + 4 * d0;
-#pragma unroll
-                for (int q = 0; q < 8; q += 2)
-                    *reinterpret_cast<uint4 *>(out + 4 * q) = make_uint4(
-                        pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv),
-                        pack_bf16x2(acc[q + 1].x * inv, acc[q + 1].y * inv),
-                        pack_bf16x2(acc[q + 1].z * inv, acc[q + 1].w * inv));
-                if (d0 == 0 && a.lse) a.lse[to * a.q_heads + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-            }
-        }
+        // the item that begins in this CTA and ends in another, if there is one
+        if (mode == kListed && tid == 0) a.parts[blockIdx.x] = part;
     }
     tc_fence_before();
     __syncthreads();
@@ -1013,6 +946,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Joins the items that several CTAs of a list had a part of, in the order of the CTAs: block (c, y)
+// the rows 64 y .. of the item that begins in CTA c. By itself and over the whole GPU: a part is
+// up to 128 KB, and joined by the last CTA to finish, six of them took 14 us. Its blocks are in
+// place before the parts are written, and wait for them.
+constexpr int kJoinRows = 64, kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_tc_join_kernel(const AttnArgs a, int tokens) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const AttnPart p = a.parts[blockIdx.x];
+    if (p.last < 0) return;
+    constexpr int kSlot = tc_slot_words(D), kEach = D / 4 / (kJoinThreads / kJoinRows);
+    const int row = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, e = row / kTile, r = row % kTile;
+    const int tl = r / a.group;
+    if (tl >= tokens || e * tokens + tl >= p.rows) return;
+    auto slot_of = [&](int k) { return a.partials + (size_t)(2 * k + (k == p.first ? 1 : 0)) * kSlot; };
+    float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+    for (int k = p.first; k <= p.last; ++k) M = fmaxf(M, __ldcg(slot_of(k) + 2 * kTile * D + 2 * row));
+    const float base = M == -INFINITY ? 0.f : M;
+    const int d0 = threadIdx.x / kJoinRows * kEach;
+    float4 acc[kEach];
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = p.first; k <= p.last; ++k) {
+        const float *sl = slot_of(k);
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kTile * D) + row);
+        const float f = ex2(ml.x - base);
+        L = fmaf(ml.y, f, L);
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(sl) + (d0 + q) * (2 * kTile) + row);
+            acc[q].x = fmaf(v.x, f, acc[q].x), acc[q].y = fmaf(v.y, f, acc[q].y);
+            acc[q].z = fmaf(v.z, f, acc[q].z), acc[q].w = fmaf(v.w, f, acc[q].w);
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int h = p.hk * a.group + r - tl * a.group;
+    const long long tok = p.row0 + e * tokens + tl;
+    uint16_t *out = a.out.p + tok * a.out.ts + h * a.out.hs + 4 * d0;
+#pragma unroll
+    for (int q = 0; q < kEach; q += 2)
+        *reinterpret_cast<uint4 *>(out + 4 * q) =
+            make_uint4(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv),
+                       pack_bf16x2(acc[q + 1].x * inv, acc[q + 1].y * inv),
+                       pack_bf16x2(acc[q + 1].z * inv, acc[q + 1].w * inv));
+    if (d0 == 0 && a.lse) a.lse[tok * a.q_heads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 template <int D, bool CAPPED>
@@ -1051,6 +1034,23 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     if (mode != kOneItem && grid > sms) grid = sms;
     err = launch_kernel(attn_tc_kernel<D, CAPPED>, dim3((unsigned)grid), dim3(kThreads), (size_t)TcShape<D>::kSmem, stream,
                         1, mk, mv, a, tokens, mode);
+    if (err != cudaSuccess) return err;
+    err = cudaGetLastError();
+    if (err != cudaSuccess || mode != kListed || grid < 2) return err;
+    // always with programmatic dependent launch: nothing is read before the wait
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    const int rows = (int)std::min((long long)a.m.max_q * a.group, 2ll * kTile);
+    // rows of a pair are spread over its two halves
+    const int blocks = rows > tokens * a.group ? 2 * kTile / kJoinRows : (rows + kJoinRows - 1) / kJoinRows;
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)blocks);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D>, a, tokens);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
