@@ -56,9 +56,10 @@ def _heads(name: str, t: _Tensor, dev: int, n=None, h=None, d=None) -> bytes:
     raise _refuse(name, t, _BF16, (n, h, d), "[tokens, heads, head_dim]")
 
 
-def _new(like: _Tensor, shape) -> tuple[_Tensor, bytes]:
+def _new(like: _Tensor, shape: torch.Size) -> tuple[_Tensor, bytes]:
     """A new contiguous bf16 [tokens, heads, head_dim] tensor beside `like`, and its fd_heads."""
-    t = torch.empty(shape, dtype=_BF16, device=like.device)
+    # (the likeness of a dense tensor is the cheaper call)
+    t = torch.empty_like(like) if like.is_contiguous() else torch.empty(shape, dtype=_BF16, device=like.device)
     n, h, d = shape
     return t, _HEADS.pack(t.data_ptr(), h * d, d, h)
 
@@ -74,17 +75,21 @@ def _flat(name: str, t: _Tensor, dev: int, dtype: torch.dtype, n=None) -> int:
 
 def _cache(k: _Tensor, v: _Tensor, dev: int) -> tuple[bytes, int, int]:
     """(fd_paged_cache, kv_heads, head_dim) of bf16 [num_pages, page_size, kv_heads, head_dim] tensors."""
+    if isinstance(k, _Tensor) and isinstance(v, _Tensor) and k.dtype is _BF16 and v.dtype is _BF16 \
+            and k.get_device() == dev >= 0 and v.get_device() == dev:
+        shape = k.shape
+        if len(shape) == 4 and v.shape == shape:
+            pages, page, heads, d = shape
+            a0, a1, a2, a3 = k.stride()
+            b0, b1, b2, b3 = v.stride()
+            if a3 == 1 and b3 == 1:
+                return (_CACHE.pack(k.data_ptr(), v.data_ptr(), a0, a1, a2, b0, b1, b2, pages, page, heads, d),
+                        heads, d)
     for name, t in (("k_cache", k), ("v_cache", v)):
         if not (isinstance(t, _Tensor) and t.dtype is _BF16 and t.get_device() == dev >= 0 and t.dim() == 4
                 and t.stride(3) == 1):
             raise _refuse(name, t, _BF16, (None,) * 4, "[num_pages, page_size, kv_heads, head_dim]")
-    shape = k.shape
-    if shape != v.shape:
-        raise ValueError(f"k_cache and v_cache differ in shape: {tuple(shape)}, {tuple(v.shape)}")
-    pages, page, heads, d = shape
-    a, b = k.stride(), v.stride()
-    return (_CACHE.pack(k.data_ptr(), v.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2], pages, page, heads, d),
-            heads, d)
+    raise ValueError(f"k_cache and v_cache differ in shape: {tuple(k.shape)}, {tuple(v.shape)}")
 
 
 def _batch(q_start, kv_len, block_table, dev: int, total_q: int, max_q: int) -> bytes:
