@@ -82,7 +82,8 @@ def test_chunks(cuda_device, q_lens, kv_lens, hq, hk, d):
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 1], [1, 100, 777]), ([9, 300], [400, 700]), ([1000], [1000])])
 @pytest.mark.parametrize("kw", [dict(window=1), dict(window=16), dict(window=200), dict(softcap=5.0),
                                 dict(window=100, softcap=30.0), dict(causal=False),
-                                dict(causal=False, window=50), dict(scale=0.5), dict(scale=-0.1)])
+                                dict(causal=False, window=50), dict(scale=0.5), dict(scale=-0.1),
+                                dict(scale=0.0), dict(softcap=0.5, scale=1.0)])
 @pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (7, 1, 64)])
 def test_options(cuda_device, q_lens, kv_lens, kw, hq, hk, d):
     checked(Batch(hq, hk, d, q_lens, kv_lens, 16, seed=3, q_std=2.0), **kw)
@@ -211,3 +212,80 @@ def test_back_to_back_with_programmatic_launch(cuda_device):
     check_attention(b, outs[0])
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+# ---------------------------------------------------------------- how the work is dealt out
+
+
+def test_many_sequences_of_chunks(cuda_device):
+    # more sequences than a CTA lists: an item a CTA, some of them empty
+    q_lens = [(7 * i) % 10 for i in range(200)]
+    kv_lens = [n + (i * i) % 150 for i, n in enumerate(q_lens)]
+    checked(Batch(8, 2, 128, q_lens, kv_lens, 16, seed=20, spare_rows=2))
+
+
+def test_many_decoded_sequences(cuda_device):
+    # several sequences for each thread of the list, some empty
+    lens = [0 if i % 7 == 3 else 1 + (i * 37) % 90 for i in range(1500)]
+    checked(Batch(4, 1, 64, [1 if t else 0 for t in lens], lens, 16, seed=21))
+
+
+def test_more_pairs_than_a_list(cuda_device):
+    # 32 heads a key head: four tokens a half
+    checked(Batch(32, 1, 64, [700, 650, 1, 0, 33], [700, 900, 50, 3, 33], 32, seed=22))
+
+
+@pytest.mark.parametrize("q_len,kv", [(20, 20000), (130, 9001), (40, 3000)])
+@pytest.mark.parametrize("hq,hk,d", [(4, 1, 128), (8, 2, 64)])
+def test_one_chunk_over_many_ctas(cuda_device, q_len, kv, hq, hk, d):
+    # the joining of many parts of few items
+    checked(Batch(hq, hk, d, [q_len], [kv], 64, seed=kv, q_std=2.0))
+
+
+def test_parts_without_keys(cuda_device):
+    # long caches of which a window leaves little, and rows that see nothing among rows that do
+    checked(Batch(4, 1, 128, [200, 60], [5000, 40], 64, seed=23), window=100)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([5, 1, 2], [300, 20, 2]), ([1, 1], [4000, 17])])
+def test_more_query_heads_than_a_tile(cuda_device, q_lens, kv_lens):
+    checked(Batch(130, 1, 64, q_lens, kv_lens, 16, seed=24, spare_rows=1))
+
+
+@pytest.mark.parametrize("q_len", [1, 90])
+@pytest.mark.parametrize("cap", [1.0, 8.0, 200.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_caps_inside_and_beyond_the_scores(cuda_device, q_len, cap, d):
+    # every score far below the cap, every one far above it, and both in one tile
+    for std in (0.2, 6.0):
+        b = Batch(8, 2, d, [q_len, q_len], [400, 150], 16, seed=25, q_std=std)
+        checked(b, softcap=cap)
+
+
+def test_heads_and_pages_of_one(cuda_device):
+    # dimensions of one entry, whatever their strides say
+    b = Batch(3, 1, 128, [1, 17], [15, 16], 16, seed=26)
+    b.k_cache = b.k_cache.as_strided(b.k_cache.shape, (b.k_cache.stride(0), b.k_cache.stride(1), 999, 1))
+    checked(b)
+    one = Batch(4, 2, 64, [5], [16], 16, seed=27, max_pages=1)
+    page = one.slots[0][0][:1]
+    one.k_cache, one.v_cache = one.k_cache[page].contiguous(), one.v_cache[page].contiguous()
+    one.block_table.fill_(0)
+    checked(one)
+
+
+def test_refusals_of_the_binding(cuda_device):
+    b = Batch(4, 2, 128, [1, 1], [20, 30])
+    scratch = fd.paged_attention_scratch(2, 2, 4, 2, 128, 1)
+    ok = dict(q=b.q, k_cache=b.k_cache, v_cache=b.v_cache, q_start=b.q_start, kv_len=b.kv_len,
+              block_table=b.block_table, max_q=1, scratch=scratch)
+    fd.paged_attention(**ok)
+    for change, error in ((dict(q=b.q.float()), TypeError), (dict(q=b.q[0]), ValueError), (dict(q=b.q[:, :3]), ValueError),
+                          (dict(kv_len=b.kv_len.long()), TypeError), (dict(q_start=b.q_start[:2]), ValueError),
+                          (dict(block_table=b.block_table.cpu()), ValueError), (dict(max_q=-1), ValueError),
+                          (dict(k_cache=b.k_cache[..., :64]), ValueError), (dict(scratch=scratch[:100]), fd.FdError),
+                          (dict(out=b.q[:1]), ValueError), (dict(lse=torch.zeros(2, 3, device="cuda")), ValueError),
+                          (dict(k_cache=b.k_cache.transpose(2, 3)), ValueError), (dict(window=-2), ValueError),
+                          (dict(out=b.q), fd.FdError), (dict(scale=float("nan")), fd.FdError)):
+        with pytest.raises(error):
+            fd.paged_attention(**{**ok, **change})
