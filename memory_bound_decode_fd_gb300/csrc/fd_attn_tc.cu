@@ -50,8 +50,8 @@ static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kT
 constexpr int kMaxListed = kAttnTcListed;  // pairs, and sequences, of one list
 // How the work is dealt out (launch_d).
 enum { kOneItem, kListed, kPersistent };
-// How scores become exponents (softmax steps).
-enum { kPlain, kSmallCap, kGeneral };
+// How scores are capped: not at all, all of a warp's below half the cap or below the cap, any.
+enum { kNoCap, kNearCap, kBelowCap, kAnyCap };
 constexpr float kRaise = 8.f;        // log2 units
 // In tiles: what beginning an item costs (its queries loaded, the last result written), and what
 // joining the parts of one costs, at all and for each part of 256 rows (128 KB written and read
@@ -76,14 +76,19 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// tanh(y) / y as a polynomial in y^2, for |y| <= 1: the minimax one of degree 7 (found by exchange
-// on a fine grid); with the rounding of its steps tanh(y) is off by at most 1.4 2^-24.
+// tanh(y) / y as a polynomial in z = y^2: the minimax ones (found by exchange on a fine grid) for
+// |y| <= 1/2, degree 4, and |y| <= 1, degree 7; with the rounding of its steps tanh(y) is off by at
+// most 1.4 2^-24.
+template <bool NEAR>
 __device__ __forceinline__ float2 tanh_over(float2 z) {
-    const float c[8] = {1.0f, -0.3333328366f, 0.1333224028f, -0.0538756959f,
-                        0.0214784257f, -0.0079373326f, 0.0022966541f, -0.0003574573f};
-    float2 p = make_float2(c[7], c[7]);
+    constexpr int kDegree = NEAR ? 4 : 7;
+    const float near[8] = {1.0f, -0.3333306909f, 0.1332477927f, -0.0529860742f, 0.0171350073f};
+    const float below[8] = {1.0f, -0.3333328366f, 0.1333224028f, -0.0538756959f,
+                            0.0214784257f, -0.0079373326f, 0.0022966541f, -0.0003574573f};
+    auto c = [&](int i) { return NEAR ? make_float2(near[i], near[i]) : make_float2(below[i], below[i]); };
+    float2 p = c(kDegree);
 #pragma unroll
-    for (int i = 6; i >= 0; --i) p = ffma2(p, z, make_float2(c[i], c[i]));
+    for (int i = kDegree - 1; i >= 0; --i) p = ffma2(p, z, c(i));
     return p;
 }
 
@@ -718,18 +723,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pin<32>(u);
                         if (masked) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(seen[c] >> k & 1)) u[k] = 0xFF800000u;  // -infinity
+                            for (int k = 0; k < 32; ++k) {
+                                const bool see = seen[c] >> k & 1;
+                                // how far from 0 the lowest one is
+                                if (CAPPED && see) size = fmaxf(size, -__uint_as_float(u[k]));
+                                if (!see) u[k] = 0xFF800000u;  // -infinity
+                            }
+                        } else if (CAPPED) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2)
+                                size = fmaxf(fmaxf(size, -__uint_as_float(u[k])), -__uint_as_float(u[k + 1]));
                         }
 #pragma unroll
                         for (int k = 0; k < 32; k += 2)
                             mx[k >> 1 & 3] = fmaxf(fmaxf(mx[k >> 1 & 3], __uint_as_float(u[k])), __uint_as_float(u[k + 1]));
-                        if (CAPPED) {
-                            // how far from 0 the lowest one is, the hidden ones set aside
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (seen[c] >> k & 1) size = fmaxf(size, -__uint_as_float(u[k]));
-                        }
                         if (c == 1) last_score = u[31];
                     }
                     const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -780,27 +787,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Groups of 16 columns, one behind the other: the exponentials of a group are issued
                 // between the sums and roundings of the one before, whose results have arrived by
                 // then. Left together the compiler waits for each of them.
-                auto step = [&](auto kind, uint32_t *su, const uint32_t *done, int n) {
+                auto step = [&](auto cap, auto hidden, uint32_t *su, const uint32_t *done, int n) {
                     float *y = reinterpret_cast<float *>(su);
                     const float *v = reinterpret_cast<const float *>(done);
+                    constexpr int kCap = decltype(cap)::value;
                     uint32_t p[8];
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
                         if (n < 4) {
                             float2 f = make_float2(y[k], y[k + 1]);
-                            if constexpr (decltype(kind)::value == kPlain) {
+                            if constexpr (kCap == kNoCap) {
                                 f = ffma2(f, make_float2(mul, mul), make_float2(off, off));
+                            } else if constexpr (kCap == kAnyCap) {
+                                f.x = log2_score(f.x) + off, f.y = log2_score(f.y) + off;
                             } else {
-                                if constexpr (!CAPPED) {
-                                    f = ffma2(f, make_float2(mul, mul), make_float2(off, off));
-                                } else if constexpr (decltype(kind)::value == kSmallCap) {
-                                    const float2 zero = make_float2(0.f, 0.f);
-                                    f = ffma2(f, make_float2(cap_in, cap_in), zero);
-                                    const float2 t = tanh_over(ffma2(f, f, zero));
-                                    f = ffma2(ffma2(f, make_float2(cap_out, cap_out), zero), t, make_float2(off, off));
-                                } else {
-                                    f.x = log2_score(f.x) + off, f.y = log2_score(f.y) + off;
-                                }
+                                const float2 zero = make_float2(0.f, 0.f);
+                                f = ffma2(f, make_float2(cap_in, cap_in), zero);
+                                const float2 t = tanh_over<kCap == kNearCap>(ffma2(f, f, zero));
+                                f = ffma2(ffma2(f, make_float2(cap_out, cap_out), zero), t, make_float2(off, off));
+                            }
+                            if constexpr (decltype(hidden)::value) {
                                 const uint32_t see = seen[(16 * n + k) >> 5] >> ((16 * n + k) & 31);
                                 f.x = see & 1 ? f.x : -INFINITY;
                                 f.y = see & 2 ? f.y : -INFINITY;
@@ -827,35 +833,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[e][part]);
                 };
-                auto steps = [&](auto kind) {
-                    step(kind, v0, v0, 0);
-                    step(kind, v1, v0, 1);
+                auto steps = [&](auto cap, auto hidden) {
+                    step(cap, hidden, v0, v0, 0);
+                    step(cap, hidden, v1, v0, 1);
                     tmem_ld_x16(s_addr + 32, v0);
                     tmem_ld_wait();
                     pin<16>(v0);
-                    step(kind, v0, v1, 2);
+                    step(cap, hidden, v0, v1, 2);
                     tmem_ld_x16(s_addr + 48, v1);
                     hand_over(0);
                     tmem_ld_wait();
                     pin<16>(v1);
-                    step(kind, v1, v0, 3);
-                    step(kind, v1, v1, 4);
+                    step(cap, hidden, v1, v0, 3);
+                    step(cap, hidden, v1, v1, 4);
                 };
                 // Each case by itself, without a branch from its first load to its last store; the cap
                 // by a polynomial where all of the warp's scores are below it, else by an exponential
                 // and a quotient (three prompts of up to 2500 tokens, capped, in a window of 512: 100 us
                 // with the polynomial, 141 without).
-                if constexpr (!CAPPED) {
-                    if (!masked)
-                        steps(std::integral_constant<int, kPlain>{});
+                auto with_cap = [&](auto cap) {
+                    if (masked)
+                        steps(cap, std::true_type{});
                     else
-                        steps(std::integral_constant<int, kGeneral>{});
-                } else {
-                    if (__all_sync(0xFFFFFFFFu, size * cap_in <= 1.f))
-                        steps(std::integral_constant<int, kSmallCap>{});
-                    else
-                        steps(std::integral_constant<int, kGeneral>{});
-                }
+                        steps(cap, std::false_type{});
+                };
+                if constexpr (!CAPPED)
+                    with_cap(std::integral_constant<int, kNoCap>{});
+                else if (__all_sync(0xFFFFFFFFu, size * cap_in <= 0.5f))
+                    with_cap(std::integral_constant<int, kNearCap>{});
+                else if (__all_sync(0xFFFFFFFFu, size * cap_in <= 1.f))
+                    with_cap(std::integral_constant<int, kBelowCap>{});
+                else
+                    steps(std::integral_constant<int, kAnyCap>{}, std::true_type{});
                 hand_over(1);
                 l2 = fadd2(l2, fadd2(la, lb));
             }
