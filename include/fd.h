@@ -1,7 +1,7 @@
 /*
  * fd.h - C ABI of the fused memory-bound decode kernels for GB300 (sm_103a).
  *
- * Two operations of an LLM decode layer, each one kernel launch:
+ * Operations of an LLM decode layer, each one kernel launch (fd_paged_attention of chunks: two):
  *
  *   fd_swiglu_w4a16_gemv   y = (silu(g) * u) . dequant(W_int4)^T   ("GEMM prologue
  *                          fusion": the activation and the int4 dequantisation are done
@@ -23,6 +23,11 @@
  *                          tensor cores' block-scaled MMA.
  *   fd_decode_mlp_step     a whole decode step (add-RMSNorm + down projection per layer)
  *                          as one persistent launch, bit-identical to the chain of calls.
+ *   fd_rope                rotary positions on queries and keys.
+ *   fd_rope_append         the same on a batch's QKV rows, the keys and values written to their
+ *                          places in a paged cache.
+ *   fd_paged_attention     attention over that cache: single tokens, chunks of prompts, or both
+ *                          in one batch.
  *
  * Sources (web pages, cited by title and section):
  *   [FIX]  "PyTorch Community Proposes Fusion Fix as Large Intermediate Buffers May Slow
@@ -43,7 +48,8 @@
  *
  * Conventions shared by every entry point
  *   - Every tensor pointer is a DEVICE pointer (cudaMalloc / PyTorch CUDA memory) on the
- *     current device, contiguous, row-major, 16-byte aligned. The caller allocates and
+ *     current device, contiguous, row-major, 16-byte aligned (of rotary positions and the paged
+ *     cache: with the strides and alignments given there). The caller allocates and
  *     owns every buffer. The library allocates no memory and keeps no state beyond a
  *     per-device cache of the SM count.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream). Calls are
@@ -540,8 +546,9 @@ int fd_rope(const fd_heads *q, const fd_heads *k, const fd_heads *q_out, const f
  * q, k, v    [total_q] tokens; k and v have cache->kv_heads heads. q_out as in fd_rope.
  * positions  int32 [total_q], or NULL: the token's number in its cache.
  * A token whose number is negative (kv_len below the number of new tokens: a padded sequence of
- * a captured batch may have kv_len 0) has no place and is not written; one at or past
- * max_pages * page_size is not written and sets FD_DEVICE_STATUS_BAD_PAGE. Two sequences must not
+ * a captured batch may have kv_len 0) has no place and is not written. Of a sequence whose kv_len
+ * is above max_pages * page_size nothing is written, and FD_DEVICE_STATUS_BAD_PAGE is set. max_q
+ * is not used. Two sequences must not
  * write the same place of a shared page in one call. The cache may not overlap itself, q, k, v or
  * q_out.
  */
@@ -569,16 +576,23 @@ int fd_rope_append(const fd_heads *q, const fd_heads *k, const fd_heads *v, cons
  * Keys past kv_len, and what else lies in their pages, may hold anything, NaN included. Keys and
  * values below kv_len must be finite where a later token of the same call sees them.
  * Scores and probabilities: fp32 scores, maximum, sum and accumulator; each probability is
- * rounded to bf16 for its product with v; one rounding of the result.
- * Requires  q_heads a multiple of kv_heads, scale finite, window >= 0, softcap >= 0 and finite.
- *           total_q == 0 or batch == 0 is an empty call: FD_OK at once, no pointer read.
+ * rounded to bf16 for its product with v; one rounding of the result. A score's error is some
+ * 2^-24 of its size (as of any fp32 sum), so that of scores past 10^6 nothing is left to tell apart:
+ * such a call's results are undefined.
+ * Requires  q_heads a multiple of kv_heads, window >= 0, softcap >= 0; softcap, |scale| and, with
+ *           a softcap, |scale| / softcap at most 1e30 (FD_ERR_UNSUPPORTED).
+ *           total_q, batch or max_q 0 is an empty call: FD_OK at once, no pointer read.
+ * Chunks (max_q * q_heads / kv_heads > 16) run on the tensor cores' fifth generation where the
+ * scale is positive and no more than 128 heads share a key head, else 16 rows at a time, many
+ * times slower.
  */
 int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_paged_batch *batch,
                        const fd_heads *out, float *lse, float scale, int causal, int window,
                        float softcap, void *scratch, size_t scratch_bytes, fd_stream_t stream);
 
-/* Bytes of scratch that suffice for every fd_paged_attention call whose batch, total_q, heads,
- * head_dim and max_q are at most these (host only; 0 for a size that the call refuses). */
+/* Bytes of scratch that suffice for every fd_paged_attention call with these heads and head_dim
+ * whose batch, total_q and max_q are at most these (host only; 0 for a size that the call refuses):
+ * 4 MB at most for single tokens, 67 MB where max_q * q_heads / kv_heads > 16. */
 size_t fd_paged_attention_scratch_bytes(int batch, int total_q, int q_heads, int kv_heads,
                                         int head_dim, int max_q);
 

@@ -13,6 +13,7 @@ namespace {
 
 constexpr long long kMaxStride = 1ll << 36;  // elements; a tensor map's strides end at 2^40 bytes
 constexpr int kMaxTokens = 1 << 28;
+constexpr float kMaxScale = 1e30f;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -316,7 +317,11 @@ int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_
     if (!cache || !batch) return FD_ERR_NULL;
     if (!std::isfinite(scale) || window < 0 || !(softcap >= 0.f) || !std::isfinite(softcap))
         return FD_ERR_SHAPE;
-    if (batch->total_q == 0 || batch->batch == 0) return FD_OK;  // empty: nothing read or written
+    // what the kernels make of them stays finite
+    if (std::fabs(scale) > kMaxScale || (softcap > 0.f && (softcap > kMaxScale || std::fabs(scale) / softcap > kMaxScale)))
+        return FD_ERR_UNSUPPORTED;
+    // empty: nothing read or written
+    if (batch->total_q == 0 || batch->batch == 0 || batch->max_q == 0) return FD_OK;
     if (!q || !out || !scratch) return FD_ERR_NULL;
     Dim dk[3], dv[3];
     long long kb = 0, vb = 0;

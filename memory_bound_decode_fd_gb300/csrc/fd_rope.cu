@@ -143,7 +143,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                     const int at = kv - (a.m.q_start[b + 1] - first) + ((int)t - first);
                     k.pos = at;
                     k.state = 1;
-                    if (at >= 0 && at < a.m.capacity) {
+                    if (a.m.kv_len[b] > a.m.capacity) {  // its tokens would go over others'
+                        atomicOr(&g_page_status, (unsigned)FD_DEVICE_STATUS_BAD_PAGE);
+                    } else if (at >= 0) {
                         const int page = a.m.table[(long long)b * a.m.table_stride + (at >> a.m.page_shift)];
                         if (page >= 0 && page < a.m.num_pages) {
                             const int off = at & ((1 << a.m.page_shift) - 1);

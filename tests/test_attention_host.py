@@ -165,6 +165,8 @@ def attend(lib, q=heads(Q), c=cache(), b=batch(), o=heads(O), lse=L, scale=0.1, 
     (dict(b=batch(total_q=0), q=None, s=None), OK), (dict(b=batch(batch=0), o=None), OK),
     (dict(q=None), NULL), (dict(o=None), NULL), (dict(s=None), NULL), (dict(c=None), NULL), (dict(b=None), NULL),
     (dict(scale=math.inf), SHAPE), (dict(window=-1), SHAPE), (dict(cap=-1.0), SHAPE), (dict(cap=math.nan), SHAPE),
+    (dict(scale=2e30), UNSUP), (dict(scale=-2e30), UNSUP), (dict(cap=2e30), UNSUP), (dict(cap=1e-32), UNSUP),
+    (dict(b=batch(max_q=0), q=None, o=None), OK),
     (dict(cap=math.inf), SHAPE), (dict(n=1000), SHAPE), (dict(q=heads(Q, 4096, 128, 20), o=heads(O, 4096, 128, 20)), SHAPE),
     (dict(o=heads(O, n=16)), SHAPE), (dict(c=cache(page=48)), SHAPE), (dict(b=batch(max_q=-1)), SHAPE),
     (dict(c=cache(d=256)), UNSUP), (dict(s=S + 8), ALIGN), (dict(lse=L + 2), ALIGN), (dict(q=heads(Q + 4)), ALIGN),

@@ -289,3 +289,27 @@ def test_refusals_of_the_binding(cuda_device):
                           (dict(out=b.q), fd.FdError), (dict(scale=float("nan")), fd.FdError)):
         with pytest.raises(error):
             fd.paged_attention(**{**ok, **change})
+
+
+def test_no_new_tokens_at_all(cuda_device):
+    b = Batch(4, 2, 64, [1, 2], [30, 40])
+    out = torch.full_like(b.q, 5.0)
+    scratch = fd.paged_attention_scratch(2, 3, 4, 2, 64, 0)
+    fd.paged_attention(b.q, *b.args(), 0, scratch, out=out)
+    torch.cuda.synchronize()
+    assert bool((out == 5.0).all())
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_a_cap_far_below_all_scores(cuda_device, q_len):
+    b = Batch(4, 1, 64, [q_len], [70], seed=31)
+    v = b.values[0].double()[:, 0]
+    i = torch.arange(70 - q_len, 70, device="cuda")
+    # a cap so small that all visible keys count the same
+    out, lse = run(b, scale=1.0, softcap=1e-30)
+    n = (i + 1).double()
+    mean = v.cumsum(0)[i] / n[:, None]
+    room = v.abs().cumsum(0)[i] / n[:, None]
+    # each probability and the result rounded to bf16 once, sums of 70 in fp32
+    assert bool(((out[:q_len].double() - mean[:, None]).abs() <= (2.0**-8 * room + 2.0**-8 * mean.abs() + 1e-5)[:, None]).all())
+    assert torch.allclose(lse[:q_len].double(), n.log()[:, None].expand(-1, 4), atol=1e-5)

@@ -166,6 +166,20 @@ def test_append_without_a_place(cuda_device):
     check_rope(q_out, q, torch.tensor([-1, 16, 31], device="cuda"), f, 64, False, 1.0)
 
 
+def test_append_past_the_table_writes_nothing(cuda_device):
+    # all pages there, one token more than they hold: no place, and no other's place either
+    b = Batch(2, 1, 64, [2, 1], [32, 20], page=16)
+    b.kv_len = torch.tensor([33, 20], dtype=torch.int32, device="cuda")
+    kc = b.k_cache.clone()
+    q, k, v = normal((3, 2, 64), 1), normal((3, 1, 64), 2), normal((3, 1, 64), 3)
+    f, _ = fd.rope_inv_freq(64, device="cuda")
+    fd.device_status()
+    fd.rope_append(q, k, v, *b.args(), f)
+    assert fd.device_status() == fd.FD_DEVICE_STATUS_BAD_PAGE
+    changed = (b.k_cache.view(torch.int16) != kc.view(torch.int16)).any(-1).flatten().nonzero().tolist()
+    assert changed == [[int(b.block_table[1, 1]) * 16 + 3]]
+
+
 def test_append_offsets_past_32_bits(cuda_device):
     # a cache of more than 2^31 elements, its last pages used
     hk, d, page = 8, 128, 64
