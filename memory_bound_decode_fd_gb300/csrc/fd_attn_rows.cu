@@ -249,9 +249,27 @@ __global__ void __launch_bounds__(RowsShape<D>::kThreads, 1)
         deal.total = (long long)all * deal.items;
         const long long n = (long long)a.m.batch * deal.items;
         const int c = blockIdx.x;
-        // whole items one after the other, or equal runs of tiles joined where they meet
-        const long long rounds = (n + gridDim.x - 1) / gridDim.x;
-        deal.whole = n < (1ll << 31) && rounds * most * gridDim.x <= deal.total + (long long)kJoinTiles * gridDim.x;
+        // Whole items one after the other, or equal runs of tiles joined where they meet: what a CTA
+        // gets of the first at most, counted, or estimated where that would take long.
+        const int G = gridDim.x;
+        long long share = most;
+        if (n > 16 * G) {
+            share = deal.total / G + 3 * most;
+        } else if (n > G) {
+            unsigned *const of = reinterpret_cast<unsigned *>(merge);  // not in use yet
+            for (int i = tid; i < kAttnMaxCtas; i += kThreads) of[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < (int)n; i += kThreads) {
+                const int b = i / deal.items;
+                atomicAdd(&of[i % G], prefix[b + 1] - prefix[b]);
+            }
+            __syncthreads();
+            unsigned m = 0;
+            for (int i = lane; i < kAttnMaxCtas; i += 32) m = max(m, of[i]);
+            share = __reduce_max_sync(0xFFFFFFFFu, m);
+            __syncthreads();
+        }
+        deal.whole = n < (1ll << 31) && share * G <= deal.total + (long long)kJoinTiles * G;
         if (deal.whole) {
             deal.G = gridDim.x;
             deal.begin = c, deal.end = n;
