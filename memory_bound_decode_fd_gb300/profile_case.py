@@ -6,6 +6,8 @@
     python -m memory_bound_decode_fd_gb300.profile_case rmsnorm --rows 8192 --hidden 4096
     python -m memory_bound_decode_fd_gb300.profile_case gate_up --K 4096 --N 14336
     python -m memory_bound_decode_fd_gb300.profile_case nvfp4 --M 64 --K 4096 --N 6144
+    python -m memory_bound_decode_fd_gb300.profile_case rope_append --batch 4 --tokens 2048 --kv 2048
+    python -m memory_bound_decode_fd_gb300.profile_case attention --batch 64 --tokens 1 --kv 4096
 
 Each iteration uses the next of --sets input sets, so that consecutive launches do not
 find their weights in L2. Exits 0 after a final synchronize.
@@ -31,7 +33,8 @@ def main(argv=None) -> int:
     from memory_bound_decode_fd_gb300 import build, inputs
 
     ap = argparse.ArgumentParser()
-    ap.add_argument("case", choices=["gemv", "gemv_residual", "rmsnorm", "gate_up", "nvfp4"])
+    ap.add_argument("case", choices=["gemv", "gemv_residual", "rmsnorm", "gate_up", "nvfp4", "rope_append",
+                                     "attention"])
     ap.add_argument("--M", type=int, default=1)
     ap.add_argument("--K", type=int, default=14336)
     ap.add_argument("--N", type=int, default=4096, help="rows (gate_up: I, the stacked weight has 2I)")
@@ -39,6 +42,15 @@ def main(argv=None) -> int:
     ap.add_argument("--rows", type=int, default=8192)
     ap.add_argument("--hidden", type=int, default=4096)
     ap.add_argument("--eps", type=float, default=1e-6)
+    ap.add_argument("--batch", type=int, default=1, help="sequences of the paged batch")
+    ap.add_argument("--tokens", type=int, default=1, help="new tokens of each")
+    ap.add_argument("--kv", type=int, default=4096, help="tokens of each in the cache, the new ones included")
+    ap.add_argument("--heads", type=int, default=32)
+    ap.add_argument("--kv-heads", type=int, default=8)
+    ap.add_argument("--head-dim", type=int, default=128)
+    ap.add_argument("--page", type=int, default=64)
+    ap.add_argument("--softcap", type=float, default=0.0)
+    ap.add_argument("--window", type=int, default=0)
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--sets", type=int, default=2)
     ap.add_argument("--path", choices=sorted(["auto", "cuda_core", "bulk", "tensor"]), default="auto")
@@ -84,6 +96,32 @@ def main(argv=None) -> int:
         for i in range(args.iters):
             x, xs, w, ws = sets[i % len(sets)]
             fd.nvfp4_scaled_mm(x, xs, w, ws, alpha, out=out)
+    elif args.case in ("rope_append", "attention"):
+        B, T, H, HK, D = args.batch, args.tokens, args.heads, args.kv_heads, args.head_dim
+        per, n = -(-args.kv // args.page), B * T
+        gen = torch.Generator(device=dev).manual_seed(0)
+
+        def normal(*shape):
+            return torch.randn(shape, generator=gen, device=dev).to(torch.bfloat16)
+
+        i32 = dict(dtype=torch.int32, device=dev)
+        q_start, kv_len = torch.arange(0, n + 1, T, **i32), torch.full((B,), args.kv, **i32)
+        inv_freq, _ = fd.rope_inv_freq(D, device=dev)
+        scratch = fd.paged_attention_scratch(B, n, H, HK, D, T)
+        sets = []
+        for i in range(args.sets):
+            table = torch.randperm(B * per, generator=gen, device=dev).to(torch.int32).view(B, per)
+            sets.append((normal(n, H + 2 * HK, D), normal(B * per, args.page, HK, D),
+                         normal(B * per, args.page, HK, D), table))
+        out = torch.empty((n, H, D), dtype=torch.bfloat16, device=dev)
+        for i in range(args.iters):
+            qkv, kc, vc, table = sets[i % len(sets)]
+            q, k, v = qkv[:, :H], qkv[:, H:H + HK], qkv[:, H + HK:]
+            if args.case == "rope_append":
+                fd.rope_append(q, k, v, kc, vc, q_start, kv_len, table, inv_freq, q_out=out)
+            else:
+                fd.paged_attention(q, kc, vc, q_start, kv_len, table, T, scratch, softcap=args.softcap,
+                                   window=args.window, out=out)
     else:
         sets = []
         for i in range(args.sets):
