@@ -5,14 +5,20 @@
 // takes 2 x 128 of them (two halves of floor(128 / group) tokens), so that each tile of keys and
 // values, copied once, serves all the heads that share it. Per tile of 128 keys and half:
 //     S = Q K^T (128 x 128 in tensor memory),  P = exp(S - m),  O = O + P V (in tensor memory).
-// Bound by the tensor cores: 4 * 128 * 128 * D flops a tile and half; the exponentials come next
-// (128 x 128 of them, half the tensor time at D = 128, all of it at D = 64).
+// Bound by the tensor cores: 4 * 128 * 128 * D flops a tile and half. A prompt of 8192 (32 heads on
+// 8, D 128) takes 380 us: 1450 TFLOP/s, 76 % of what a large matrix product reaches; 512 tokens
+// behind 16000 118 us, 1155 TFLOP/s. A CTA spends 3600 cycles on a tile of both halves: the 32
+// MMAs take 70 each, 2250 in all (64 at the tensor cores' full rate), and for the rest the tensor
+// cores wait for probabilities, a half's softmax (1600 cycles, latencies more than issue slots) being
+// longer than the other half's MMAs (1130). At D = 64 the MMAs are shorter and the softmax is not:
+// 700 TFLOP/s. Tiles of 64 keys, whose scores can be ready before they are wanted, need more and
+// shorter MMAs: 500 us.
 //
 //   * One warp copies key and value tiles (tensor-map copies of a page's 64-element columns) into a
-//     ring, one warp issues the MMAs, and two groups of four warps do the softmax of one half each,
-//     one row a thread. While one half is in the softmax the tensor cores run the other's P V and
-//     next S: per tile the MMA warp issues, for each half in turn, P V of this tile and then S of
-//     the next, and never waits for its own results.
+//     ring, one warp issues the MMAs, one deals out the work, and two groups of eight warps do the
+//     softmax of one half each, two threads a row. While one half is in the softmax the tensor cores
+//     run the other's P V and next S: per tile the MMA warp issues, for each half in turn, P V of
+//     this tile and then S of the next, and never waits for its own results.
 //   * S, P and O stay in tensor memory: P (bf16, two a column) takes the first half of S's
 //     columns and is the A operand of the second product from there. MMAs run in the order of
 //     issue, so the next S may overwrite P without a wait. Q and both operands of S are
@@ -23,8 +29,10 @@
 //     relative at most), the row's sum is that of the unrounded values, in fp32.
 //   * Work: up to kMaxListed pairs of halves and the grid is one CTA an SM, which deals itself
 //     items (a pair and a key head), or, where whole items do not come out even, equal runs of the
-//     tiles of all items; what several CTAs share is joined by a second kernel. With more sequences
-//     than a CTA lists, each takes one item, the longest first.
+//     tiles of all items; what several CTAs share is joined by a second kernel (512 tokens behind
+//     16000: 118 us, 241 in whole items). More pairs than that are whole items in any case (a prompt
+//     of 8192: 376 and 380 us). With more sequences than a CTA lists, each CTA takes one item, the
+//     longest first (100 chunks of 40 behind 1000: 105 us, 94 by the list).
 //   * Values of the first and last tile that no row of the item sees are cleared in shared memory
 //     before their MMA (0 x NaN): pages hold anything past the last token.
 //   * Every wait is bounded; a CTA that gives up writes NaN, drains its copies and MMAs and frees
@@ -848,9 +856,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     step(cap, hidden, v1, v1, 4);
                 };
                 // Each case by itself, without a branch from its first load to its last store; the cap
-                // by a polynomial where all of the warp's scores are below it, else by an exponential
-                // and a quotient (three prompts of up to 2500 tokens, capped, in a window of 512: 100 us
-                // with the polynomial, 141 without).
+                // by a polynomial where all of the warp's scores are below it, a shorter one where they
+                // are below half of it, else by an exponential and a quotient (three prompts of up to 2500
+                // tokens, capped, in a window of 512: 80 us; 98 with the longer polynomial alone, 141 with
+                // neither).
                 auto with_cap = [&](auto cap) {
                     if (masked)
                         steps(cap, std::true_type{});
@@ -958,10 +967,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the items that several CTAs of a list had a part of, in the order of the CTAs: block (c, y)
-// the rows 64 y .. of the item that begins in CTA c. By itself and over the whole GPU: a part is
+// the rows 32 y .. of the item that begins in CTA c. By itself and over the whole GPU: a part is
 // up to 128 KB, and joined by the last CTA to finish, six of them took 14 us. Its blocks are in
 // place before the parts are written, and wait for them.
-constexpr int kJoinRows = 64, kJoinThreads = 256;
+constexpr int kJoinRows = 32, kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_tc_join_kernel(const AttnArgs a, int tokens) {
     grid_dep_wait();
