@@ -366,7 +366,10 @@ int fd_gemv_uses_tensor_cores(int M, int K, int N, int group);
  * fd_decode_mlp_step under this flag: the same short limit, and one CTA never adds itself to
  * the first layer's count, so every CTA's wait for that count runs out; layer 0's y and
  * normalised row are correct, every later output and the residual are NaN, and the status
- * reports FD_DEVICE_STATUS_WAIT_TIMEOUT. */
+ * reports FD_DEVICE_STATUS_WAIT_TIMEOUT.
+ * fd_paged_attention under this flag: the same short limit, and the first keys of every CTA are
+ * never copied; every row that sees a key is NaN, the status reports FD_DEVICE_STATUS_WAIT_TIMEOUT,
+ * and the scratch is ready for the next call. */
 #define FD_LAUNCH_TEST_WAIT_TIMEOUT 512u
 int fd_set_launch_flags(unsigned flags);
 unsigned fd_get_launch_flags(void);

@@ -70,6 +70,8 @@ struct AttnArgs {
     unsigned *counters;  // one per CTA, zero between calls
     float *partials;     // one slot for the first and one for the last item of each CTA
     struct AttnPart *parts;  // of fd_attn_tc.cu: one for each CTA
+    // FD_LAUNCH_TEST_WAIT_TIMEOUT: short waits, and the first copy of every CTA is left out.
+    int test_timeout;
 };
 // An item that begins in one CTA and ends in another (last < 0: there is none).
 struct AttnPart {

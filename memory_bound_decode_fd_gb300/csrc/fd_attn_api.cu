@@ -356,6 +356,7 @@ int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_
     a.head_dim = d, a.causal = causal != 0;
     a.window = window > 2 * FD_MAX_SEQ ? 2 * FD_MAX_SEQ : window;
     a.scale = scale, a.softcap = softcap;
+    a.test_timeout = (launch_flags() & FD_LAUNCH_TEST_WAIT_TIMEOUT) != 0;
     a.counters = static_cast<unsigned *>(scratch);
     a.partials = reinterpret_cast<float *>(static_cast<unsigned char *>(scratch) + kAttnCounterBytes);
     const bool tc = attn_uses_tc(a.m.max_q, a.group, scale);

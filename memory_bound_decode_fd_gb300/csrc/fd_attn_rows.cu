@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(RowsShape<D>::kThreads, 1)
     }
 
     const uint32_t ring = smem_u32(smem) + warp * S::kRing;
+    const long long wait_limit = a.test_timeout ? kTestWaitLimitCycles : kWaitLimitCycles;
     if (tid >= S::kConsumers) {
         // ---------------------------------------------------------------------- copies
         const uint64_t policy = policy_evict_first();
@@ -340,9 +341,9 @@ __global__ void __launch_bounds__(RowsShape<D>::kThreads, 1)
             if (hk < 0) break;
             __syncwarp();
             describe(entry);
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[warp][slot], phase, &abort_flag));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[warp][slot], phase, &abort_flag, wait_limit));
             if (!ok) break;
-            if (lane == 0) {
+            if (lane == 0 && !(a.test_timeout && warp == 0 && issued == 0)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if ((read >> i & 1) && (unsigned)page[i] >= (unsigned)a.m.num_pages)
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(RowsShape<D>::kThreads, 1)
             for (uint32_t i = issued - n; i < issued; ++i) {
                 const long long t0 = clock64();
                 while (!mbar_try_parity(&full[warp][i % S::kStages], (i / S::kStages) & 1u) &&
-                       clock64() - t0 < kWaitLimitCycles) {
+                       clock64() - t0 < wait_limit) {
                 }
             }
         }
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(RowsShape<D>::kThreads, 1)
 
 #pragma unroll 1
         for (int t = g.from; t < g.to; ++t) {
-            if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[warp][stage], phase, &abort_flag));
+            if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[warp][stage], phase, &abort_flag, wait_limit));
             if (dead) break;
             const uint32_t kb = ring + stage * 2 * S::kPart, vb = kb + S::kPart;
             uint64_t *const done = &empty[warp][stage];

@@ -107,21 +107,23 @@ __device__ __forceinline__ void pin(uint32_t *r) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+__device__ __forceinline__ long long wait_limit(int test) { return test ? kTestWaitLimitCycles : kWaitLimitCycles; }
+
 // Bounded wait that ignores the abort flag (copies landing, MMAs completing).
-__device__ __forceinline__ void wait_hw(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ void wait_hw(uint64_t *bar, uint32_t parity, int test) {
     const long long t0 = clock64();
-    while (!mbar_try_parity(bar, parity) && clock64() - t0 < kWaitLimitCycles) {
+    while (!mbar_try_parity(bar, parity) && clock64() - t0 < wait_limit(test)) {
     }
 }
 
 // mbar_wait_bounded with the slow path in line: a call would bind this kernel's registers to the
 // calling convention, which a kernel that moves registers between its warps has none left for.
-__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int test) {
     if (mbar_try_parity(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_try_parity(bar, parity)) {
         if (*abort_flag) return false;
-        if (clock64() - t0 > kWaitLimitCycles) {
+        if (clock64() - t0 > wait_limit(test)) {
             *abort_flag = 1;
             record_wait_timeout();
             return false;
@@ -344,11 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int off = (j * kTile + my_box * box) & ((1 << a.m.page_shift) - 1);
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    ok = __all_sync(0xFFFFFFFFu, wait_bounded(&empty[stage], phase ^ 1u, &abort_flag));
+                    ok = __all_sync(0xFFFFFFFFu, wait_bounded(&empty[stage], phase ^ 1u, &abort_flag, a.test_timeout));
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&full[stage], T::kStage);
+                    const bool copy = !(a.test_timeout && issued == 0);
+                    if (copy && lane == 0) mbar_arrive_expect_tx(&full[stage], T::kStage);
                     __syncwarp();
-                    if (lane < ops) {
+                    if (copy && lane < ops) {
                         const MapOrder ord = v ? a.ov : a.ok;
                         const int y1 = ord.tok == 1 ? off : ord.head == 1 ? hk : page;
                         const int y2 = ord.tok == 2 ? off : ord.head == 2 ? hk : page;
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0) {  // wait (bounded) for the copies in flight before the CTA ends
             const uint32_t n = issued < (uint32_t)T::kStages ? issued : (uint32_t)T::kStages;
             for (uint32_t i = issued - n; i < issued; ++i)
-                wait_hw(&full[i % T::kStages], (i / T::kStages) & 1u);
+                wait_hw(&full[i % T::kStages], (i / T::kStages) & 1u, a.test_timeout);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (!__all_sync(0xFFFFFFFFu, mbar_try_parity(bar, parity)))
-                ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, &abort_flag));
+                ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, &abort_flag, a.test_timeout));
             return ok;
         };
         auto scores = [&](int e, int st) {  // S_e = Q_e K^T
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) {  // nothing may be in flight when the memory is given back
             tc_commit(&done);
-            wait_hw(&done, 0);
+            wait_hw(&done, 0, a.test_timeout);
         }
         __syncwarp();
     } else if (warp == kDealWarp) {
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = jb > ja && !dead;
             const int j0 = ja;
             for (int j = ja; j < jb && !dead; ++j) {
-                const bool ok = __all_sync(0xFFFFFFFFu, wait_bounded(&s_full[e], s_ph, &abort_flag));
+                const bool ok = __all_sync(0xFFFFFFFFu, wait_bounded(&s_full[e], s_ph, &abort_flag, a.test_timeout));
                 s_ph ^= 1u;
                 tc_fence_after();
                 // Half of the scores are read twice, for their maximum and for the exponentials: tensor
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l = l2.x + l2.y;
             if (any) {
                 // the other half of the row's sum, by way of the scores' first columns, now free
-                const bool ok = !dead && __all_sync(0xFFFFFFFFu, wait_bounded(&o_full[e], o_ph, &abort_flag));
+                const bool ok = !dead && __all_sync(0xFFFFFFFFu, wait_bounded(&o_full[e], o_ph, &abort_flag, a.test_timeout));
                 o_ph ^= 1u;
                 tc_fence_after();
                 tmem_st_x1(s_addr, __float_as_uint(l));

@@ -6,6 +6,7 @@ import torch
 
 import memory_bound_decode_fd_gb300 as fd
 from attn_check import Batch, check_attention
+from memory_bound_decode_fd_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -313,3 +314,28 @@ def test_a_cap_far_below_all_scores(cuda_device, q_len):
     # each probability and the result rounded to bf16 once, sums of 70 in fp32
     assert bool(((out[:q_len].double() - mean[:, None]).abs() <= (2.0**-8 * room + 2.0**-8 * mean.abs() + 1e-5)[:, None]).all())
     assert torch.allclose(lse[:q_len].double(), n.log()[:, None].expand(-1, 4), atol=1e-5)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 1], [5000, 3, 700]), ([300, 2], [4000, 90]), ([40] * 200, [50] * 200)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_wait_that_runs_out_is_reported(cuda_device, q_lens, kv_lens, d):
+    # a copy that is never made (the launch flag for it): no fault, no hang, and the scratch as good
+    # as before
+    lib = fd.load_library()
+    b = Batch(8, 2, d, q_lens, kv_lens, 16, seed=33)
+    scratch = fd.paged_attention_scratch(len(q_lens), b.q.shape[0], 8, 2, d, b.max_q)
+    run(b, scratch)
+    assert fd.device_status() == 0
+    flags = lib.fd_get_launch_flags()
+    assert lib.fd_set_launch_flags(flags | _lib.FD_LAUNCH_TEST_WAIT_TIMEOUT) == _lib.FD_OK
+    try:
+        out, lse = run(b, scratch)
+        torch.cuda.synchronize()
+    finally:
+        lib.fd_set_launch_flags(flags)
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    assert fd.device_status() == _lib.FD_DEVICE_STATUS_WAIT_TIMEOUT
+    assert fd.device_status() == 0
+    out, lse = run(b, scratch)
+    check_attention(b, out, lse)
+    assert fd.device_status() == 0
