@@ -104,9 +104,9 @@ cudaError_t launch_attn_tc(const AttnArgs &a, const CUtensorMap &mk, const CUten
                            cudaStream_t stream);
 cudaError_t status_attn_tc(cudaStream_t stream, unsigned *out, bool clear);
 
-// Which of the two: up to 16 rows a key head are one pass of the first (16 sequences of 8 new
-// tokens and 4 heads a key head, 32 rows: 78 us in two passes of the first, 58 in the second); a
-// group of more than 128 query heads does not fit the second's tile, and it wants a positive scale.
+// Which of the two: up to 16 rows a key head are one pass of the first (16 sequences of up to 6000,
+// 4 heads a key head: 4 new tokens, 16 rows, 51 us in the first and 65 in the second; 8, 32 rows, 78
+// in two passes of the first and 51 in the second); a group of more than 128 query heads does not fit the second's tile, and it wants a positive scale.
 inline bool attn_uses_tc(int max_q, int group, float scale) {
     return (long long)max_q * group > kRowsM && group <= kAttnTcTile && scale > 0.f;
 }

@@ -6,13 +6,13 @@
 // values, copied once, serves all the heads that share it. Per tile of 128 keys and half:
 //     S = Q K^T (128 x 128 in tensor memory),  P = exp(S - m),  O = O + P V (in tensor memory).
 // Bound by the tensor cores: 4 * 128 * 128 * D flops a tile and half. A prompt of 8192 (32 heads on
-// 8, D 128) takes 380 us: 1450 TFLOP/s, 76 % of what a large matrix product reaches; 512 tokens
-// behind 16000 118 us, 1155 TFLOP/s. A CTA spends 3600 cycles on a tile of both halves: the 32
+// 8, D 128) takes 369 us: 1490 TFLOP/s, 78 % of what a large matrix product reaches; 512 tokens
+// behind 16000 118 us, 1150 TFLOP/s. A CTA spends 3500 cycles on a tile of both halves: the 32
 // MMAs take 70 each, 2250 in all (64 at the tensor cores' full rate), and for the rest the tensor
 // cores wait for probabilities, a half's softmax (1600 cycles, latencies more than issue slots) being
 // longer than the other half's MMAs (1130). At D = 64 the MMAs are shorter and the softmax is not:
 // 700 TFLOP/s. Tiles of 64 keys, whose scores can be ready before they are wanted, need more and
-// shorter MMAs: 500 us.
+// shorter MMAs: 500 us for that prompt.
 //
 //   * One warp copies key and value tiles (tensor-map copies of a page's 64-element columns) into a
 //     ring, one warp issues the MMAs, one deals out the work, and two groups of eight warps do the
@@ -31,7 +31,7 @@
 //     items (a pair and a key head), or, where whole items do not come out even, equal runs of the
 //     tiles of all items; what several CTAs share is joined by a second kernel (512 tokens behind
 //     16000: 118 us, 241 in whole items). More pairs than that are whole items in any case (a prompt
-//     of 8192: 376 and 380 us). With more sequences than a CTA lists, each CTA takes one item, the
+//     of 8192, with a list long enough and without: 380 and 376 us). With more sequences than a CTA lists, each CTA takes one item, the
 //     longest first (100 chunks of 40 behind 1000: 105 us, 94 by the list).
 //   * Values of the first and last tile that no row of the item sees are cleared in shared memory
 //     before their MMA (0 x NaN): pages hold anything past the last token.
@@ -400,10 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        auto commit = [&](uint64_t *bar) {
-            if (elect_one()) tc_commit(bar);
-            __syncwarp();
-        };
+        auto commit = [&](uint64_t *bar) { tc_commit_if(elect_one(), bar); };
         for (int n = 0;; ++n) {
             const volatile Segment &g = take(n);
             if (!same(g.valid)) break;
@@ -450,25 +447,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j >= ha[e] && j < hb[e]) {
                         // The first 32 keys of both 64s as soon as their probabilities are there, then
                         // the other ones.
+                        // Predicated, not in a branch on the elected lane like the scores (a prompt of
+                        // 8192: 367 us, 380 with both in branches, 370 with both predicated).
+                        const bool issue = elect_one();
                         auto values = [&](int k, uint32_t accumulate) {  // keys 16 k ..
-                            tc_mma_f16_ts(tm + T::kO0 + e * kTile, tm + T::kS0 + e * kTile + (k >> 2) * 64 + (k & 3) * 8,
-                                          desc_of(vd + k * (2048 >> 4)), idesc_o, accumulate);
+                            tc_mma_f16_ts_if(issue, tm + T::kO0 + e * kTile,
+                                             tm + T::kS0 + e * kTile + (k >> 2) * 64 + (k & 3) * 8,
+                                             desc_of(vd + k * (2048 >> 4)), idesc_o, accumulate);
                         };
                         if (!wait(&p_full[e][0], p_ph[e])) break;
                         tc_fence_after();
-                        if (elect_one()) {
-                            values(0, j > ha[e]);
-                            values(1, 1), values(4, 1), values(5, 1);
-                        }
-                        __syncwarp();
+                        values(0, j > ha[e]);
+                        values(1, 1), values(4, 1), values(5, 1);
                         if (!wait(&p_full[e][1], p_ph[e])) break;
                         p_ph[e] ^= 1u;
                         tc_fence_after();
-                        if (elect_one()) {
-                            values(2, 1), values(3, 1), values(6, 1), values(7, 1);
-                            if (j + 1 == hb[e]) tc_commit(&o_full[e]);
-                        }
-                        __syncwarp();
+                        values(2, 1), values(3, 1), values(6, 1), values(7, 1);
+                        if (j + 1 == hb[e]) tc_commit_if(issue, &o_full[e]);
                     }
                     if (e == 1) commit(&empty[vs]);
                     if (more) {
