@@ -219,8 +219,8 @@ def rope_append(
 def paged_attention_scratch(batch: int, total_q: int, q_heads: int, kv_heads: int, head_dim: int,
                             max_q: int, device=None) -> torch.Tensor:
     """A zeroed scratch buffer for ``paged_attention`` calls with these heads and head_dim and at
-    most these batch, total_q and max_q; every completed call leaves it ready for the next. One per stream (and per graph that may run at
-    the same time as another)."""
+    most these batch, total_q and max_q; every completed call leaves it ready for the next. One per
+    stream (and per graph that may run at the same time as another)."""
     n = _lib.load().fd_paged_attention_scratch_bytes(batch, total_q, q_heads, kv_heads, head_dim, max_q)
     if n == 0:
         raise ValueError("paged_attention does not take these sizes (see fd_paged_attention in include/fd.h)")

@@ -106,7 +106,8 @@ cudaError_t status_attn_tc(cudaStream_t stream, unsigned *out, bool clear);
 
 // Which of the two: up to 16 rows a key head are one pass of the first (16 sequences of up to 6000,
 // 4 heads a key head: 4 new tokens, 16 rows, 51 us in the first and 65 in the second; 8, 32 rows, 78
-// in two passes of the first and 51 in the second); a group of more than 128 query heads does not fit the second's tile, and it wants a positive scale.
+// in two passes of the first and 51 in the second); a group of more than 128 query heads does not
+// fit the second's tile, and it wants a positive scale.
 inline bool attn_uses_tc(int max_q, int group, float scale) {
     return (long long)max_q * group > kRowsM && group <= kAttnTcTile && scale > 0.f;
 }
