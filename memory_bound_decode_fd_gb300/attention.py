@@ -3,6 +3,7 @@ key/value cache and the attention over it. Argument marshalling only, like kerne
 
 from __future__ import annotations
 
+import ctypes
 import struct
 
 import torch
@@ -11,8 +12,10 @@ from . import _lib
 from .kernels import _on_device, _stream_handle
 
 # These calls are a few microseconds on the GPU when decoding, so what the host does for them
-# counts: checks read each attribute once, structures are packed without ctypes objects, and what
-# exactly is wrong with an argument is looked into only when something is.
+# counts. Calls whose arguments are plainly in order are made by csrc/fd_torch.cpp (_fast); the
+# others, and all where it has not been built, here: checks read each attribute once, structures
+# are packed without ctypes objects, and what exactly is wrong with an argument is looked into only
+# when something is.
 
 _Tensor, _BF16, _I32 = torch.Tensor, torch.bfloat16, torch.int32
 
@@ -20,6 +23,25 @@ _Tensor, _BF16, _I32 = torch.Tensor, torch.bfloat16, torch.int32
 _HEADS = struct.Struct("=Qqqi4x")
 _CACHE = struct.Struct("=QQqqqqqqiiii")
 _BATCH = struct.Struct("=QQQiiiii4x")
+
+_fast = None  # csrc/fd_torch.cpp, from the first call on (False: not built)
+
+
+def _load():
+    """The library; its first call also loads the C++ form of the calls below."""
+    global _fast
+    lib = _lib.load()
+    if _fast is None:
+        try:
+            from . import _fd_torch
+
+            _fd_torch.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                             for f in (lib.fd_rope, lib.fd_rope_append, lib.fd_paged_attention)))
+            _fast = _fd_torch
+        except ImportError:
+            _fast = False
+    return lib
+
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -148,6 +170,11 @@ def rope(
     (2i, 2i + 1) if interleaved, else (i, i + rot_dim / 2). q_out, k_out: allocated if None; q
     and k themselves for a rotation in place.
     """
+    if _fast and stream is None:
+        r = _fast.rope(q, k, positions, inv_freq, interleaved, scale, q_out, k_out)
+        if r is not None:
+            return r if r.__class__ is tuple else _lib.check(r)
+    lib = _load()
     dev = _device(q)
     qb = _heads("q", q, dev)
     shape = n, _, d = q.shape
@@ -166,7 +193,7 @@ def rope(
         q_out, qo = _new(q, shape)
     else:
         qo = _heads("q_out", q_out, dev, *shape)
-    _call(dev, _lib.load().fd_rope, qb, kb, qo, ko, pos, freq, n, d, rot, 1 if interleaved else 0, scale,
+    _call(dev, lib.fd_rope, qb, kb, qo, ko, pos, freq, n, d, rot, 1 if interleaved else 0, scale,
           _stream(stream, dev))
     return q_out, k_out
 
@@ -198,6 +225,12 @@ def rope_append(
     in its cache). q_out: allocated if None; may be q (in place). Rows past q_start[batch] are not
     written.
     """
+    if _fast and stream is None:
+        r = _fast.rope_append(q, k, v, k_cache, v_cache, q_start, kv_len, block_table, inv_freq, positions,
+                              interleaved, scale, q_out)
+        if r is not None:
+            return r if r.__class__ is _Tensor else _lib.check(r)
+    lib = _load()
     dev = _device(q)
     cache, hk, d = _cache(k_cache, v_cache, dev)
     qb = _heads("q", q, dev, None, None, d)
@@ -211,7 +244,7 @@ def rope_append(
         q_out, qo = _new(q, shape)
     else:
         qo = _heads("q_out", q_out, dev, *shape)
-    _call(dev, _lib.load().fd_rope_append, qb, kb, vb, qo, cache, batch, pos, freq, rot,
+    _call(dev, lib.fd_rope_append, qb, kb, vb, qo, cache, batch, pos, freq, rot,
           1 if interleaved else 0, scale, _stream(stream, dev))
     return q_out
 
@@ -256,6 +289,12 @@ def paged_attention(
     q_heads] output, the log of each row's sum of exponentials. A row that sees no key gives zeros
     and -inf.
     """
+    if _fast and stream is None:
+        r = _fast.paged_attention(q, k_cache, v_cache, q_start, kv_len, block_table, max_q, scratch, scale, causal,
+                                  window, softcap, out, lse)
+        if r is not None:
+            return r if r.__class__ is _Tensor else _lib.check(r)
+    lib = _load()
     dev = _device(q)
     cache, hk, d = _cache(k_cache, v_cache, dev)
     qb = _heads("q", q, dev, None, None, d)
@@ -276,7 +315,7 @@ def paged_attention(
                 or lse.shape != shape[:2] or not lse.is_contiguous():
             raise _refuse("lse", lse, torch.float32, (n, h), "contiguous [total_q, q_heads]")
         lse_ptr = lse.data_ptr()
-    _call(dev, _lib.load().fd_paged_attention, qb, cache, batch, ob, lse_ptr,
+    _call(dev, lib.fd_paged_attention, qb, cache, batch, ob, lse_ptr,
           d**-0.5 if scale is None else scale, 1 if causal else 0, min(window, 2**31 - 1), softcap, work,
           scratch.shape[0], _stream(stream, dev))
     return out

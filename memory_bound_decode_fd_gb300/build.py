@@ -4,6 +4,10 @@ Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into one sh
 library next to this file. The CUDA runtime is linked statically, so the library needs
 only the NVIDIA driver at run time. ``build()`` is a no-op when the library is newer
 than every source and header.
+
+``csrc/fd_torch.cpp`` becomes ``_fd_torch.so``, the C++ form of attention.py's calls, against
+the headers of the torch that is installed. Where those or Python's are missing it is left out,
+and the calls do the same in Python.
 """
 
 from __future__ import annotations
@@ -12,6 +16,8 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 from pathlib import Path
 
 PKG_DIR = Path(__file__).resolve().parent
@@ -20,6 +26,9 @@ CSRC = PKG_DIR / "csrc"
 INCLUDE = REPO_DIR / "include"
 BUILD_DIR = REPO_DIR / "_build"
 LIB_PATH = PKG_DIR / "libfd.so"
+TORCH_SRC = CSRC / "fd_torch.cpp"
+TORCH_PATH = PKG_DIR / "_fd_torch.so"
+TORCH_STAMP = BUILD_DIR / "fd_torch.torch"  # the torch that TORCH_PATH was built against
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{INCLUDE}"]
@@ -49,6 +58,45 @@ def is_stale() -> bool:
     return any(p.stat().st_mtime > lib_mtime for p in _deps())
 
 
+def _torch_version() -> str | None:
+    try:
+        import torch
+    except ImportError:
+        return None
+    return f"{torch.__version__} {sys.version}"
+
+
+def _torch_stale() -> bool:
+    if not TORCH_PATH.exists() or not TORCH_STAMP.exists() or TORCH_STAMP.read_text() != _torch_version():
+        return True
+    made = TORCH_PATH.stat().st_mtime
+    return any(p.stat().st_mtime > made for p in (TORCH_SRC, INCLUDE / "fd.h"))
+
+
+def _build_torch(verbose: bool) -> None:
+    """``_fd_torch.so``, or none where it cannot be built."""
+    version, python = _torch_version(), sysconfig.get_path("include")
+    TORCH_PATH.unlink(missing_ok=True)
+    if version is None or not Path(python, "Python.h").exists():
+        return
+    import torch
+
+    root = Path(torch.__file__).parent
+    cuda = Path(_nvcc()).resolve().parent.parent
+    tmp = TORCH_PATH.with_suffix(".so.tmp")
+    try:
+        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
+              f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}", f"-I{python}",
+              f"-I{cuda / 'include'}", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+              str(TORCH_SRC), "-o", str(tmp), f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+              "-lc10"], verbose)
+    except (RuntimeError, OSError) as e:
+        print(f"_fd_torch.so not built, attention.py's calls stay in Python: {e}", file=sys.stderr)
+        return
+    os.replace(tmp, TORCH_PATH)
+    TORCH_STAMP.write_text(version)
+
+
 def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -63,10 +111,18 @@ def _run(cmd: list[str], verbose: bool) -> None:
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> Path:
     """Compile and link ``libfd.so``; return its path."""
-    if not force and not is_stale():
-        return LIB_PATH
-    nvcc = _nvcc()
     BUILD_DIR.mkdir(exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        beside = ex.submit(_build_torch, verbose) if force or _torch_stale() else None
+        if force or is_stale():
+            _build_lib(verbose, ptxas_info)
+        if beside:
+            beside.result()
+    return LIB_PATH
+
+
+def _build_lib(verbose: bool, ptxas_info: bool) -> None:
+    nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     jobs = []
     for src in _sources():
@@ -77,10 +133,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     tmp = LIB_PATH.with_suffix(".so.tmp")
     _run([nvcc, *ARCH_FLAGS, "-shared", "-o", str(tmp), *[str(o) for o, _ in jobs]], verbose)
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force="--force" in sys.argv, verbose=True, ptxas_info="--ptxas" in sys.argv))

@@ -119,3 +119,63 @@ def test_prompts_then_tokens(cuda_device, pdl):
     finally:
         fd.set_pdl(prev)
     assert fd.device_status() == 0
+
+
+def test_calls_from_python_and_from_cpp_agree(cuda_device, monkeypatch):
+    # attention.py hands a call whose arguments are in order to its C++ form, and makes it itself where
+    # that has not been built: the same results, new outputs and given ones, and the same refusals
+    from memory_bound_decode_fd_gb300 import attention
+
+    attention._load()
+    assert attention._fast, "csrc/fd_torch.cpp is not built"
+    b = Batch(4, 2, 64, [1, 5, 0], [40, 33, 0], 16, seed=3, spare_rows=1)
+    n = b.q.shape[0]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    row = torch.randn(n, 8, 64, device="cuda", generator=gen).to(torch.bfloat16)
+    k, v = row[:, 4:6], row[:, 6:]
+    inv_freq, _ = fd.rope_inv_freq(32, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    scratch = fd.paged_attention_scratch(3, n, 4, 2, 64, b.max_q)
+    caches = b.k_cache.clone(), b.v_cache.clone()
+    index = b.q_start, b.kv_len, b.block_table
+
+    def results():
+        kc, vc = caches[0].clone(), caches[1].clone()
+        new = torch.zeros(n, 4, 64, dtype=torch.bfloat16, device="cuda")
+        lse, out = torch.zeros(n, 4, device="cuda"), new.clone()
+        r = [*fd.rope(row[:, :4], k, pos, inv_freq, True, 1.5)]
+        r += [fd.rope(row[:, :4], None, pos, inv_freq)[0], *fd.rope(row[:, :4], k, pos, inv_freq, q_out=new)]
+        assert r[-2] is new
+        r += [fd.rope_append(row[:, :4], k, v, kc, vc, *index, inv_freq)[:6], kc, vc]
+        r += [fd.rope_append(row[:, :4], k, v, kc, vc, *index, inv_freq, pos, True, 2.0)[:6], kc, vc]
+        r += [fd.paged_attention(b.q, *caches, *index, b.max_q, scratch)[:6]]
+        assert fd.paged_attention(b.q, *caches, *index, b.max_q, scratch, 0.3, False, 9, 5.0, out, lse) is out
+        r += [out, lse]
+        stream = torch.cuda.current_stream()
+        r += [fd.paged_attention(b.q, *caches, *index, b.max_q, scratch, stream=stream)[:6]]
+        return [t.clone() for t in r]
+
+    def refusals():
+        got = []
+        for call in (lambda: fd.rope(row, k, pos[1:], inv_freq), lambda: fd.rope(row[..., :63], None, pos, inv_freq),
+                     lambda: fd.rope(row.float(), None, pos, inv_freq), lambda: fd.rope(row, None, pos.cpu(), inv_freq),
+                     lambda: fd.rope(row, None, pos, inv_freq, scale=float("inf")), lambda: fd.rope(3, None, pos, inv_freq),
+                     lambda: fd.rope(row[:, :4], row[:, 3:5], pos, inv_freq, q_out=row[:, :4], k_out=row[:, 3:5]),
+                     lambda: fd.rope_append(row[:, :4], k, v, caches[0], caches[0], *index, inv_freq),
+                     lambda: fd.rope_append(row[:, :4], k, v, *caches, *index, inv_freq.repeat(3)),
+                     lambda: fd.paged_attention(b.q, *caches, *index, -1, scratch),
+                     lambda: fd.paged_attention(b.q[:, :3], *caches, *index, 5, scratch),
+                     lambda: fd.paged_attention(b.q, *caches, *index, 5, scratch[:64]),
+                     lambda: fd.paged_attention(b.q, *caches, *index, 5, scratch, out=b.q),
+                     lambda: fd.paged_attention(b.q, *caches, *index, 5, scratch, lse=torch.zeros(4, n, device="cuda"))):
+            with pytest.raises((TypeError, ValueError, fd.FdError)) as e:
+                call()
+            got.append((type(e.value), str(e.value)))
+        return got
+
+    cpp, cpp_refusals = results(), refusals()
+    monkeypatch.setattr(attention, "_fast", False)
+    for x, y in zip(cpp, results()):
+        assert x.shape == y.shape and x.stride() == y.stride()
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert refusals() == cpp_refusals
