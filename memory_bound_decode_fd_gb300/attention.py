@@ -24,7 +24,7 @@ _HEADS = struct.Struct("=Qqqi4x")
 _CACHE = struct.Struct("=QQqqqqqqiiii")
 _BATCH = struct.Struct("=QQQiiiii4x")
 
-_fast = None  # csrc/fd_torch.cpp, from the first call on (False: not built)
+_fast = None  # csrc/fd_torch.cpp, from the first call on (False: not built, or against another torch)
 
 
 def _load():
@@ -34,12 +34,12 @@ def _load():
     if _fast is None:
         try:
             from . import _fd_torch
-
-            _fd_torch.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                             for f in (lib.fd_rope, lib.fd_rope_append, lib.fd_paged_attention)))
-            _fast = _fd_torch
         except ImportError:
             _fast = False
+        else:
+            _fd_torch.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                             for f in (lib.fd_rope, lib.fd_rope_append, lib.fd_paged_attention)))
+            _fast = _fd_torch if _fd_torch.torch_version == torch.__version__ else False
     return lib
 
 

@@ -87,9 +87,9 @@ def _build_torch(verbose: bool) -> None:
     try:
         _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
               f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}", f"-I{python}",
-              f"-I{cuda / 'include'}", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-              str(TORCH_SRC), "-o", str(tmp), f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
-              "-lc10"], verbose)
+              f"-I{cuda / 'include'}", f'-DFD_TORCH_VERSION="{torch.__version__}"',
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", str(TORCH_SRC), "-o", str(tmp),
+              f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], verbose)
     except (RuntimeError, OSError) as e:
         print(f"_fd_torch.so not built, attention.py's calls stay in Python: {e}", file=sys.stderr)
         return

@@ -263,4 +263,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fd_torch", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fd_torch() { return PyModule_Create(&module); }
+// `torch_version`: whose headers this was built against (its classes are used as they lie in memory).
+PyMODINIT_FUNC PyInit__fd_torch() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", FD_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}
