@@ -350,7 +350,9 @@ int fd_gemv_uses_tensor_cores(int M, int K, int N, int group);
  *                  but add-RMSNorm loads its weight row BEFORE that wait. Set this only
  *                  when no kernel that may still be running in the stream writes that
  *                  weight row (true for model weights during decode). Works inside CUDA graph
- *                  capture (the edges become programmatic dependencies).
+ *                  capture (the edges become programmatic dependencies). fd_rope,
+ *                  fd_rope_append and fd_paged_attention read nothing before the wait and may
+ *                  be launched so without this flag.
  * fd_set_launch_flags returns FD_ERR_UNSUPPORTED for unknown bits.
  */
 #define FD_LAUNCH_PDL 1u

@@ -258,12 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         pick_b = -1;
         fence_mbar_init();
     }
+    grid_dep_wait();
+    // Between the two: a kernel that holds tensor memory never waits for one that wants some.
     if (warp == kMmaWarp) {
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
     }
-    grid_dep_wait();
-    grid_dep_launch();
 
     auto pairs_of = [&](int b) { return (unsigned)((load_seq(a.m, b).rows + 2 * tokens - 1) / (2 * tokens)); };
     if (mode == kOneItem) {
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    grid_dep_launch();
 
     // The n-th run, as the dealing warp has written it down (its own waits are the shorter ones, so
     // this one ends), and that this warp is done with it.
@@ -1048,25 +1049,20 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     long long grid = pairs * a.kv_heads;
     if (mode == kListed) grid *= tiles > 0 ? tiles : 1;
     if (mode != kOneItem && grid > sms) grid = sms;
-    err = launch_kernel(attn_tc_kernel<D, CAPPED>, dim3((unsigned)grid), dim3(kThreads), (size_t)TcShape<D>::kSmem, stream,
-                        1, mk, mv, a, tokens, mode);
+    // Nothing is read before the wait, so programmatic launches are always right: 35 tokens in each of 3
+    // sequences 10.2 us a call, 12.3 without. Not of long calls by themselves: their CTAs then find
+    // their SMs in the order in which these become free (three capped prompts 84.6 us, 82.0 without).
+    const bool programmatic = mode != kPersistent || (launch_flags() & FD_LAUNCH_PDL) != 0;
+    err = launch_kernel_as(programmatic, attn_tc_kernel<D, CAPPED>, dim3((unsigned)grid), dim3(kThreads),
+                           (size_t)TcShape<D>::kSmem, stream, 1, mk, mv, a, tokens, mode);
     if (err != cudaSuccess) return err;
     err = cudaGetLastError();
     if (err != cudaSuccess || mode != kListed || grid < 2) return err;
-    // always with programmatic dependent launch: nothing is read before the wait
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
     const int rows = (int)std::min((long long)a.m.max_q * a.group, 2ll * kTile);
     // rows of a pair are spread over its two halves
     const int blocks = rows > tokens * a.group ? 2 * kTile / kJoinRows : (rows + kJoinRows - 1) / kJoinRows;
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)blocks);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D>, a, tokens);
+    err = launch_kernel_as(true, attn_tc_join_kernel<D>, dim3((unsigned)grid, (unsigned)blocks), dim3(kJoinThreads), 0,
+                           stream, 1, a, tokens);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }

@@ -31,14 +31,13 @@ unsigned launch_flags();
 int api_status(cudaError_t err);
 bool api_launch_fails();
 
-// Launches `kern` on `stream`; with FD_LAUNCH_PDL set the launch allows programmatic
-// dependent launch (the kernel may start while the previous kernel in the stream is
-// finishing; each kernel waits on griddepcontrol before it touches data that a previous
-// kernel produces).
+// Launches `kern` on `stream`; `programmatic`: with programmatic dependent launch (the kernel may
+// start while the previous kernel in the stream is finishing; each kernel waits on griddepcontrol
+// before it touches data that a previous kernel produces).
 // `cluster` > 1 launches thread-block clusters of that many CTAs along x.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                          cudaStream_t stream, int cluster, Args &&...args) {
+cudaError_t launch_kernel_as(bool programmatic, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, int cluster, Args &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -47,7 +46,7 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
     cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
     cfg.numAttrs = 0;
-    if (launch_flags() & FD_LAUNCH_PDL) {
+    if (programmatic) {
         attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
         ++cfg.numAttrs;
@@ -60,6 +59,13 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
         ++cfg.numAttrs;
     }
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+// The same, programmatic if FD_LAUNCH_PDL is set.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t stream, int cluster, Args &&...args) {
+    return launch_kernel_as((launch_flags() & FD_LAUNCH_PDL) != 0, kern, grid, block, smem, stream, cluster,
+                            static_cast<Args &&>(args)...);
 }
 
 // ------------------------------------------------------------------------------------

@@ -10,11 +10,12 @@
 // units of 16 elements of a head: two 16-byte loads and two 16-byte stores (the unit's two vectors
 // are the partners of each other: adjacent ones for interleaved pairs, rot_dim / 2 apart for halves).
 // Few tokens: one a CTA, its heads over several, so that a single token's 40 or 48 heads are not
-// one CTA's work (one token: 2.6 us against 2.9; the appends of 64: 3.6 against 4.0; no more than
+// one CTA's work (one token: 2.6 us against 2.9; the appends of 64: 3.6 against 4.0, both without
+// programmatic launches; no more than
 // two a CTA: at 600 tokens it takes 5.8 against 4.3, the angles being made in every part).
 //
-// 8191 tokens of 40 heads of 128, half of each rotated, take 30.1 us, 82 % of the copy bandwidth;
-// five prompts of up to 1639 appended 29.4, 76 %. Each thread has two units on
+// 8191 tokens of 40 heads of 128, half of each rotated, take 29.7 us, 83 % of the copy bandwidth;
+// five prompts of up to 1639 appended 29.0, 78 %. Each thread has two units on
 // their way; other depths, pass sizes and CTAs an SM took 29.5 to 46 us.
 //
 // Angle: position * inv_freq grows to 1e6 radians and more, where 32 bits leave nothing of the
@@ -296,7 +297,8 @@ cudaError_t launch_rope(const RopeArgs &a, bool append, cudaStream_t stream) {
     const size_t smem = (size_t)(a.rot_dim / 2 + 1) * sizeof(unsigned long long) +
                         (size_t)a.rot_dim * 2 * kRopeTokens * sizeof(float);
     const unsigned magic = (unsigned)(((1ull << 32) + per_head - 1) / per_head);
-    err = launch_kernel(kern, grid, dim3(kRopeThreads), smem, stream, 1, a, units_cta, magic);
+    // nothing is read before the wait: 8191 tokens one call behind the other 30.1 us, 32.9 without
+    err = launch_kernel_as(true, kern, grid, dim3(kRopeThreads), smem, stream, 1, a, units_cta, magic);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
