@@ -6,7 +6,7 @@
 // values, copied once, serves all the heads that share it. Per tile of 128 keys and half:
 //     S = Q K^T (128 x 128 in tensor memory),  P = exp(S - m),  O = O + P V (in tensor memory).
 // Bound by the tensor cores: 4 * 128 * 128 * D flops a tile and half. A prompt of 8192 (32 heads on
-// 8, D 128) takes 369 us: 1490 TFLOP/s, 78 % of what a large matrix product reaches; 512 tokens
+// 8, D 128) takes 363 us: 1515 TFLOP/s, 79 % of what a large matrix product reaches; 512 tokens
 // behind 16000 118 us, 1150 TFLOP/s. A CTA spends 3500 cycles on a tile of both halves: the 32
 // MMAs take 70 each, 2250 in all (64 at the tensor cores' full rate), and for the rest the tensor
 // cores wait for probabilities, a half's softmax (1600 cycles, latencies more than issue slots) being

@@ -10,13 +10,13 @@
 // units of 16 elements of a head: two 16-byte loads and two 16-byte stores (the unit's two vectors
 // are the partners of each other: adjacent ones for interleaved pairs, rot_dim / 2 apart for halves).
 // Few tokens: one a CTA, its heads over several, so that a single token's 40 or 48 heads are not
-// one CTA's work (one token: 2.6 us against 2.9; the appends of 64: 3.6 against 4.0, both without
-// programmatic launches; no more than
-// two a CTA: at 600 tokens it takes 5.8 against 4.3, the angles being made in every part).
+// one CTA's work (one token: 2.6 us against 2.9; the appends of 64: 3.6 against 4.0; with as many
+// parts for 600 tokens 5.8 against 4.3, the angles being made in every part; all of these without
+// programmatic launches).
 //
 // 8191 tokens of 40 heads of 128, half of each rotated, take 29.7 us, 83 % of the copy bandwidth;
-// five prompts of up to 1639 appended 29.0, 78 %. Each thread has two units on
-// their way; other depths, pass sizes and CTAs an SM took 29.5 to 46 us.
+// five prompts of up to 1639 appended 29.0, 78 %. Each thread has two units on their way; other
+// depths, pass sizes and CTAs an SM took 29.5 to 46 us.
 //
 // Angle: position * inv_freq grows to 1e6 radians and more, where 32 bits leave nothing of the
 // fraction. inv_freq / (2 pi) is taken in 64-bit floating point, its fraction made a 64-bit
