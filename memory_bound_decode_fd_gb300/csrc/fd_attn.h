@@ -85,6 +85,46 @@ constexpr int kAttnCounterBytes = 4 * 4096;   // the scratch begins with them
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// ---- scores in log2 units
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh(y) / y as a polynomial in z = y^2: the minimax ones (found by exchange on a fine grid) for
+// |y| <= 1/2, degree 4, and |y| <= 1, degree 7; with the rounding of its steps off by at most
+// 1.3 2^-24 of itself.
+template <bool NEAR>
+__device__ __forceinline__ float2 tanh_over(float2 z) {
+    constexpr int kDegree = NEAR ? 4 : 7;
+    const float near[8] = {1.0f, -0.3333306909f, 0.1332477927f, -0.0529860742f, 0.0171350073f};
+    const float below[8] = {1.0f, -0.3333328366f, 0.1333224028f, -0.0538756959f,
+                            0.0214784257f, -0.0079373326f, 0.0022966541f, -0.0003574573f};
+    auto c = [&](int i) { return NEAR ? make_float2(near[i], near[i]) : make_float2(below[i], below[i]); };
+    float2 p = c(kDegree);
+#pragma unroll
+    for (int i = kDegree - 1; i >= 0; --i) p = ffma2(p, z, c(i));
+    return p;
+}
+
+// Two scores s = scale v capped, c tanh(y) with y = s / c, in log2 units (lin = scale log2(e),
+// cap_in = scale / c, cap_out = c log2(e)). Below the cap it is s times tanh(y) / y: the error is one of
+// the score, where that of c (1 - 2 / (e^(2 y) + 1)) would be one of the cap (0.9 at c = 10^7, and of
+// scores of a few from c = 10^9 on nothing would be left). Above, tanh is no smaller than 0.76 and the
+// quotient is as good. NEAR: both are known to be below half the cap.
+template <bool NEAR>
+__device__ __forceinline__ float2 capped_log2(float2 v, float lin, float cap_in, float cap_out) {
+    const float2 zero = make_float2(0.f, 0.f);
+    const float2 y = ffma2(v, make_float2(cap_in, cap_in), zero);
+    float2 s = ffma2(ffma2(v, make_float2(lin, lin), zero), tanh_over<NEAR>(ffma2(y, y, zero)), zero);
+    if (NEAR) return s;
+    auto far = [&](float u) { return cap_out * (1.f - __fdividef(2.f, ex2(u * (2.f * kLog2e)) + 1.f)); };
+    if (fabsf(y.x) > 1.f) s.x = far(y.x);
+    if (fabsf(y.y) > 1.f) s.y = far(y.y);
+    return s;
+}
+
 // ---- attention of few rows per key head (fd_attn_rows.cu)
 constexpr int kRowsM = 16;      // query rows of one pass over the keys
 constexpr int kRowsBox = 32;    // tokens of a copy (16 where a page has no more)

@@ -78,28 +78,6 @@ struct TcShape {
     static constexpr uint32_t kS0 = 0, kO0 = 2 * kTile;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// tanh(y) / y as a polynomial in z = y^2: the minimax ones (found by exchange on a fine grid) for
-// |y| <= 1/2, degree 4, and |y| <= 1, degree 7; with the rounding of its steps tanh(y) is off by at
-// most 1.4 2^-24.
-template <bool NEAR>
-__device__ __forceinline__ float2 tanh_over(float2 z) {
-    constexpr int kDegree = NEAR ? 4 : 7;
-    const float near[8] = {1.0f, -0.3333306909f, 0.1332477927f, -0.0529860742f, 0.0171350073f};
-    const float below[8] = {1.0f, -0.3333328366f, 0.1333224028f, -0.0538756959f,
-                            0.0214784257f, -0.0079373326f, 0.0022966541f, -0.0003574573f};
-    auto c = [&](int i) { return NEAR ? make_float2(near[i], near[i]) : make_float2(below[i], below[i]); };
-    float2 p = c(kDegree);
-#pragma unroll
-    for (int i = kDegree - 1; i >= 0; --i) p = ffma2(p, z, c(i));
-    return p;
-}
-
 // Makes the registers of a tensor-memory load depend on the wait that came before.
 template <int N>
 __device__ __forceinline__ void pin(uint32_t *r) {
