@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The scale is positive (attn_uses_tc), so that what follows is monotone in S: the maximum of a
         // row is taken before scale and cap.
         const float cap_in = CAPPED ? a.scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
-        const float mul = CAPPED ? cap_in * (2.f * kLog2e) : a.scale * kLog2e;
+        const float mul = CAPPED ? cap_in * (2.f * kLog2e) : a.scale * kLog2e, lin = a.scale * kLog2e;
         // a score in log2 units; c tanh(y) = c (1 - 2 / (e^(2 y) + 1))
         auto log2_score = [&](float v) {
             return CAPPED ? cap_out - __fdividef(2.f * cap_out, ex2(v * mul) + 1.f) : v * mul;
@@ -676,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             give_q();
         }
         for (int run = 0; more; ++run) {
-            float m = -INFINITY;  // what the exponentials are taken against, log2 units
+            float m = -INFINITY;      // what the exponentials are taken against, log2 units
+            float m_seen = -INFINITY; // CAPPED: the score that it is, before scale and cap
             float2 l2 = make_float2(0.f, 0.f);
             const bool any = jb > ja && !dead;
             const int j0 = ja;
@@ -725,12 +726,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (c == 1) last_score = u[31];
                     }
                     const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    top = raw == -INFINITY ? raw : log2_score(raw);
+                    top = CAPPED || raw == -INFINITY ? raw : raw * mul;
                     size = fmaxf(size, raw);
                 }
-                // Raise the maximum: at the first keys, and when a row has grown by 2^kRaise. All of the
-                // half do it together, or none (and a wait that gave up ends the loop for all).
-                if (bar_or(bar, kHalf, !ok || (top > m && (m == -INFINITY || top - m > kRaise)))) {
+                // Raise the maximum: at the first keys, and when a row has grown by 2^kRaise (before the cap,
+                // which makes growth smaller; what it makes of the maximum is computed here alone). All of
+                // the half do it together, or none (and a wait that gave up ends the loop for all).
+                const float over = CAPPED ? (top - m_seen) * lin : top - m;  // NaN where both are -infinity
+                if (bar_or(bar, kHalf, !ok || over > kRaise)) {
                     if (bar_or(bar, kHalf, !ok)) {
                         dead = true;
                         break;
@@ -750,7 +753,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     tmem_st_x1(s_addr + 63, last_score);
                     tmem_st_wait();
-                    const float up = fmaxf(fmaxf(top, __uint_as_float(other)), m);
+                    float up = fmaxf(fmaxf(top, __uint_as_float(other)), CAPPED ? m_seen : m);
+                    if (CAPPED) {
+                        m_seen = up;
+                        if (up != -INFINITY) up = capped_log2<false>(make_float2(up, up), lin, cap_in, cap_out).x;
+                    }
                     const float f = m == -INFINITY ? 0.f : ex2(m - up);
                     m = up;
                     l2.x *= f, l2.y *= f;

@@ -52,8 +52,9 @@ def check(b, cap, scale=None, window=0):
         assert bool((err <= bound).all()), ("out", nq, t, float((err - bound).max()))
 
 
-# rows of one pass of the decoding kernel (with a negative scale several)
+# rows of one pass of the decoding kernel (with a negative scale several), and chunks
 SHAPES = [([1, 1, 1], [1, 5, 400], 0.3), ([1, 1], [4097, 130], None), ([9], [40], -0.2)]
+CHUNKS = [([40, 1], [40, 300], 0.3), ([90, 300], [400, 300], None)]
 
 
 @pytest.mark.parametrize("cap", [1e4, 1e5, 1e7, 1e10, 1e30])
@@ -62,6 +63,15 @@ SHAPES = [([1, 1, 1], [1, 5, 400], 0.3), ([1, 1], [4097, 130], None), ([9], [40]
 def test_caps_far_above_the_scores_of_tokens(cuda_device, q_lens, kv_lens, scale, d, cap):
     check(Batch(8, 2, d, q_lens, kv_lens, 16, seed=41, q_std=2.0), cap, scale)
     check(Batch(8, 2, d, q_lens, kv_lens, 16, seed=42, q_std=2.0), cap, scale, window=1)
+
+
+@pytest.mark.parametrize("cap", [5.0, 1e4, 1e7, 1e10, 1e30])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens,kv_lens,scale", CHUNKS)
+def test_caps_far_above_the_scores_of_chunks(cuda_device, q_lens, kv_lens, scale, d, cap):
+    # ordinary scores, and ones of about 100 (of which 2^s does not fit 32 bits)
+    for std in (2.0, 40.0):
+        check(Batch(8, 2, d, q_lens, kv_lens, 16, seed=43, q_std=std), cap, scale)
 
 
 @pytest.mark.parametrize("q_lens,kv_lens", [([4], [60])])
