@@ -583,7 +583,8 @@ int fd_rope_append(const fd_heads *q, const fd_heads *k, const fd_heads *v, cons
  * Scores and probabilities: fp32 scores, maximum, sum and accumulator; each probability is
  * rounded to bf16 for its product with v; one rounding of the result. A score's error is some
  * 2^-24 of its size (as of any fp32 sum), so that of scores past 10^6 nothing is left to tell apart:
- * such a call's results are undefined.
+ * such a call's results are undefined. The cap adds some 2^-24 of the capped score; in chunks, with a
+ * softcap of at most 1024, up to 2^-21 of the softcap where scores beside it pass the cap.
  * Requires  q_heads a multiple of kv_heads, window >= 0, softcap >= 0; softcap, |scale| and, with
  *           a softcap, |scale| / softcap at most 1e30 (FD_ERR_UNSUPPORTED).
  *           total_q, batch or max_q 0 is an empty call: FD_OK at once, no pointer read.

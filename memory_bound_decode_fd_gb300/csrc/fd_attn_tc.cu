@@ -58,7 +58,13 @@ static_assert(kSoftmax * kSoftmaxRegs + (kThreads - kSoftmax) * kOtherRegs <= kT
 constexpr int kMaxListed = kAttnTcListed;  // pairs, and sequences, of one list
 // How the work is dealt out (launch_d).
 enum { kOneItem, kListed, kPersistent };
-// How scores are capped: not at all, all of a warp's below half the cap or below the cap, any.
+// The kernels for capped scores. Where a warp has scores past the cap, all of its scores in that tile
+// are c (1 - 2 / (e^(2 y) + 1)), off by 6 2^-24 of the cap; of a cap of kLargeCap 4 10^-4, a tenth of a
+// probability's rounding. Past that, those below the cap go by the polynomial there too (two prompts of
+// 2048 in 28 heads of 64 capped at 3: 114 us, 157 so).
+enum { kUncapped, kUsualCaps, kLargeCaps };
+constexpr float kLargeCap = 1024.f;
+// How a tile's scores are capped: not at all, all of a warp's below half the cap or below the cap, any.
 enum { kNoCap, kNearCap, kBelowCap, kAnyCap };
 constexpr float kRaise = 8.f;        // log2 units
 // In tiles: what beginning an item costs (its queries loaded, the last result written), and what
@@ -192,12 +198,13 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool any) {
     return r != 0;
 }
 
-// CAPPED: the scores go through the tanh (apart, so that its code costs the others no registers).
-template <int D, bool CAPPED>
+// CAP: whether the scores go through the tanh (apart, so that its code costs the others no registers).
+template <int D, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const AttnArgs a, int tokens /* of a half */, int mode) {
     using T = TcShape<D>;
+    constexpr bool CAPPED = CAP != kUncapped;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages], done;
@@ -791,7 +798,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (kCap == kNoCap) {
                                 f = ffma2(f, make_float2(mul, mul), make_float2(off, off));
                             } else if constexpr (kCap == kAnyCap) {
-                                f.x = log2_score(f.x) + off, f.y = log2_score(f.y) + off;
+                                if constexpr (CAP == kLargeCaps)
+                                    f = fadd2(capped_log2<false>(f, lin, cap_in, cap_out), make_float2(off, off));
+                                else
+                                    f.x = log2_score(f.x) + off, f.y = log2_score(f.y) + off;
                             } else {
                                 const float2 zero = make_float2(0.f, 0.f);
                                 f = ffma2(f, make_float2(cap_in, cap_in), zero);
@@ -1000,7 +1010,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tc_join_kernel(const AttnAr
     if (d0 == 0 && a.lse) a.lse[tok * a.q_heads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-template <int D, bool CAPPED>
+template <int D, int CAP>
 cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     DeviceInfo di;
@@ -1013,10 +1023,10 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     if (dev >= 64 || !(attr_done.load(std::memory_order_acquire) & bit)) {
         // the warps' register shares wait for one another if the launch brings fewer
         cudaFuncAttributes fa;
-        err = cudaFuncGetAttributes(&fa, attn_tc_kernel<D, CAPPED>);
+        err = cudaFuncGetAttributes(&fa, attn_tc_kernel<D, CAP>);
         if (err != cudaSuccess) return err;
         if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-        err = cudaFuncSetAttribute(attn_tc_kernel<D, CAPPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        err = cudaFuncSetAttribute(attn_tc_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    TcShape<D>::kSmem);
         if (err != cudaSuccess) return err;
         if (dev < 64) attr_done.fetch_or(bit, std::memory_order_acq_rel);
@@ -1038,7 +1048,7 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
     // sequences 10.2 us a call, 12.3 without. Not of long calls by themselves: their CTAs then find
     // their SMs in the order in which these become free (three capped prompts 84.6 us, 82.0 without).
     const bool programmatic = mode != kPersistent || (launch_flags() & FD_LAUNCH_PDL) != 0;
-    err = launch_kernel_as(programmatic, attn_tc_kernel<D, CAPPED>, dim3((unsigned)grid), dim3(kThreads),
+    err = launch_kernel_as(programmatic, attn_tc_kernel<D, CAP>, dim3((unsigned)grid), dim3(kThreads),
                            (size_t)TcShape<D>::kSmem, stream, 1, mk, mv, a, tokens, mode);
     if (err != cudaSuccess) return err;
     err = cudaGetLastError();
@@ -1056,9 +1066,13 @@ cudaError_t launch_d(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap
 
 cudaError_t launch_attn_tc(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                            cudaStream_t stream) {
-    if (a.softcap > 0.f)
-        return a.head_dim == 128 ? launch_d<128, true>(a, mk, mv, stream) : launch_d<64, true>(a, mk, mv, stream);
-    return a.head_dim == 128 ? launch_d<128, false>(a, mk, mv, stream) : launch_d<64, false>(a, mk, mv, stream);
+    auto launch = [&](auto cap) {
+        constexpr int kCap = decltype(cap)::value;
+        return a.head_dim == 128 ? launch_d<128, kCap>(a, mk, mv, stream) : launch_d<64, kCap>(a, mk, mv, stream);
+    };
+    if (a.softcap > kLargeCap) return launch(std::integral_constant<int, kLargeCaps>{});
+    if (a.softcap > 0.f) return launch(std::integral_constant<int, kUsualCaps>{});
+    return launch(std::integral_constant<int, kUncapped>{});
 }
 
 FD_DEFINE_STATUS_ACCESSOR(status_attn_tc)

@@ -74,7 +74,7 @@ def test_caps_far_above_the_scores_of_chunks(cuda_device, q_lens, kv_lens, scale
         check(Batch(8, 2, d, q_lens, kv_lens, 16, seed=43, q_std=std), cap, scale)
 
 
-@pytest.mark.parametrize("q_lens,kv_lens", [([4], [60])])
+@pytest.mark.parametrize("q_lens,kv_lens", [([4], [60]), ([40], [90])])
 @pytest.mark.parametrize("d", [64, 128])
 def test_small_scores_beside_ones_past_the_cap(cuda_device, q_lens, kv_lens, d):
     # one token's scores pass the cap, the other rows' are ordinary: these lose nothing by it
