@@ -803,10 +803,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 else
                                     f.x = log2_score(f.x) + off, f.y = log2_score(f.y) + off;
                             } else {
+                                // (s tanh(y) / y, as in capped_log2: y may be 0 where s is not)
                                 const float2 zero = make_float2(0.f, 0.f);
-                                f = ffma2(f, make_float2(cap_in, cap_in), zero);
-                                const float2 t = tanh_over<kCap == kNearCap>(ffma2(f, f, zero));
-                                f = ffma2(ffma2(f, make_float2(cap_out, cap_out), zero), t, make_float2(off, off));
+                                const float2 z = ffma2(f, make_float2(cap_in, cap_in), zero);
+                                const float2 t = tanh_over<kCap == kNearCap>(ffma2(z, z, zero));
+                                f = ffma2(ffma2(f, make_float2(lin, lin), zero), t, make_float2(off, off));
                             }
                             if constexpr (decltype(hidden)::value) {
                                 const uint32_t see = seen[(16 * n + k) >> 5] >> ((16 * n + k) & 31);

@@ -83,7 +83,7 @@ def test_small_scores_beside_ones_past_the_cap(cuda_device, q_lens, kv_lens, d):
     check(b, 1e4)
 
 
-@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [3, 300])])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [3, 300]), ([40], [90])])
 @pytest.mark.parametrize("d", [64, 128])
 def test_scale_far_below_the_cap(cuda_device, q_lens, kv_lens, d):
     # scale / cap is no 32-bit number, the scores are ordinary
