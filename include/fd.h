@@ -529,7 +529,7 @@ typedef struct fd_paged_batch {
  *   y[j]     = x[j]                                               j >= rot_dim
  * interleaved 0: p0 = i, p1 = i + rot_dim / 2 (the two halves of the rotated part);
  * interleaved 1: p0 = 2 i, p1 = 2 i + 1.
- * inv_freq  fp64 [rot_dim / 2] in device memory, 8-byte aligned: any stretching of the positions
+ * inv_freq  fp64 [rot_dim / 2] in device memory, 8-byte aligned, below 2^53 in size: any stretching of the positions
  *           for long contexts is in it (rope_inv_freq of the Python package makes the usual
  *           ones), `scale` is the factor on cosine and sine that goes with it (1 for none).
  * positions int32 [tokens]; any value. The angle is reduced to one turn in 64-bit fixed point, so

@@ -19,10 +19,12 @@
 // depths, pass sizes and CTAs an SM took 29.5 to 46 us.
 //
 // Angle: position * inv_freq grows to 1e6 radians and more, where 32 bits leave nothing of the
-// fraction. inv_freq / (2 pi) is taken in 64-bit floating point, its fraction made a 64-bit
-// fixed-point number u of turns, and position * u wraps in 64-bit integer arithmetic, which is the
-// reduction to one turn, exactly and for negative positions too. The remaining fraction goes to
-// sincospif in 32 bits (error 2^-24 of a half turn at most).
+// fraction. The fraction of inv_freq / (2 pi) is made a 64-bit fixed-point number u of turns, from
+// inv_freq's 53 bits and 128 of 1 / (2 pi) in integer arithmetic, so that it is off by less than 2^-64
+// of a turn whatever inv_freq is (a product in 64-bit floating point is off by up to 2^-53 of itself,
+// 2^-22 of a turn and more at position 2^31). position * u wraps, which is the reduction to one turn,
+// exactly and for negative positions too. The remaining fraction goes to sincospif in 32 bits (error
+// 2^-24 of a half turn at most).
 #include <atomic>
 
 #include "fd_attn.h"
@@ -46,6 +48,21 @@ __device__ __forceinline__ uint32_t rotate_pair(uint32_t x, float c, float s) {
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// The fraction of f / (2 pi), |f| < 2^53, as a 64-bit fixed-point number, rounded towards 0: of the
+// product of f's mantissa m and the first 128 bits of 1 / (2 pi) the bits that belong there.
+__device__ __forceinline__ unsigned long long turns_64(double f) {
+    constexpr unsigned long long kHigh = 0x28BE60DB9391054Aull, kLow = 0x7F09D5F47D4D3770ull;
+    const unsigned long long bits = (unsigned long long)__double_as_longlong(f), one = 1ull << 52;
+    const int e = (int)(bits >> 52) & 0x7FF, s = max(1075 - max(e, 1), 0);  // |f| = m 2^-s
+    const unsigned long long m = (bits & (one - 1)) | (e ? one : 0);
+    const unsigned long long carry = __umul64hi(m, kLow), w1 = carry + m * kHigh;  // bits 64 .. 127
+    const unsigned long long w2 = __umul64hi(m, kHigh) + (w1 < carry ? 1 : 0);     // 128 ..
+    const unsigned long long u = s == 0   ? w1
+                                 : s < 64 ? w1 >> s | w2 << (64 - s)
+                                          : s < 128 ? w2 >> (s - 64) : 0;
+    return bits >> 63 ? 0 - u : u;
 }
 
 // A token: element offsets of its queries, keys and values, and of where they go.
@@ -86,11 +103,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     grid_dep_wait();
     grid_dep_launch();
 
-    for (int i = tid; i < half; i += kRopeThreads) {
-        double turns = a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-        turns -= floor(turns);
-        step[i] = (unsigned long long)(turns * 18446744073709551616.0);
-    }
+    for (int i = tid; i < half; i += kRopeThreads) step[i] = turns_64(a.inv_freq[i]);
     // Those of the tokens [first, first + n) of the ones looked up.
     auto angles = [&](int first, int n, float *cs) {
         for (int i = tid; i < n * half; i += kRopeThreads) {
