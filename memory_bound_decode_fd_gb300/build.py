@@ -66,25 +66,35 @@ def _torch_version() -> str | None:
     return f"{torch.__version__} {sys.version}"
 
 
-def _torch_stale() -> bool:
-    if not TORCH_PATH.exists() or not TORCH_STAMP.exists() or TORCH_STAMP.read_text() != _torch_version():
-        return True
-    made = TORCH_PATH.stat().st_mtime
+def _torch_older(path: Path) -> bool:
+    """Whether ``path`` is older than what ``_fd_torch.so`` is made from."""
+    made = path.stat().st_mtime
     return any(p.stat().st_mtime > made for p in (TORCH_SRC, INCLUDE / "fd.h"))
 
 
+def _torch_stale() -> bool:
+    if not TORCH_PATH.exists() or not TORCH_STAMP.exists() or TORCH_STAMP.read_text() != _torch_version():
+        return True
+    return _torch_older(TORCH_PATH)
+
+
 def _build_torch(verbose: bool) -> None:
-    """``_fd_torch.so``, or none where it cannot be built."""
+    """``_fd_torch.so``. Where it cannot be built, one from before is left if it is of the present
+    sources (that it is of another torch is found when it is loaded), else removed."""
+
+    def leave_out() -> None:
+        if TORCH_PATH.exists() and _torch_older(TORCH_PATH):
+            TORCH_PATH.unlink(missing_ok=True)
+
     version, python = _torch_version(), sysconfig.get_path("include")
-    TORCH_PATH.unlink(missing_ok=True)
     if version is None or not Path(python, "Python.h").exists():
-        return
+        return leave_out()
     import torch
 
     root = Path(torch.__file__).parent
-    cuda = Path(_nvcc()).resolve().parent.parent
     tmp = TORCH_PATH.with_suffix(".so.tmp")
     try:
+        cuda = Path(_nvcc()).resolve().parent.parent
         _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
               f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}", f"-I{python}",
               f"-I{cuda / 'include'}", f'-DFD_TORCH_VERSION="{torch.__version__}"',
@@ -92,7 +102,7 @@ def _build_torch(verbose: bool) -> None:
               f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], verbose)
     except (RuntimeError, OSError) as e:
         print(f"_fd_torch.so not built, attention.py's calls stay in Python: {e}", file=sys.stderr)
-        return
+        return leave_out()
     os.replace(tmp, TORCH_PATH)
     TORCH_STAMP.write_text(version)
 

@@ -1,0 +1,56 @@
+"""Building the C++ form of the attention binding where something is missing, twice, or in several
+processes: the library's build never fails for it, and a good module is never lost."""
+
+import os
+
+import pytest
+
+from memory_bound_decode_fd_gb300 import build
+
+
+@pytest.fixture
+def module(monkeypatch, tmp_path):
+    """A module of the present sources, built against another torch; a library that is up to date."""
+    monkeypatch.setattr(build, "TORCH_PATH", tmp_path / "_fd_torch.so")
+    monkeypatch.setattr(build, "TORCH_STAMP", tmp_path / "stamp")
+    monkeypatch.setattr(build, "is_stale", lambda: False)
+    build.TORCH_PATH.write_bytes(b"before")
+    build.TORCH_STAMP.write_text("another torch")
+    return build.TORCH_PATH
+
+
+def older(path):
+    os.utime(path, (0, 0))  # than its sources
+
+
+def no_nvcc():
+    raise RuntimeError("nvcc not found")
+
+
+@pytest.mark.parametrize("why", ["no nvcc", "no headers", "no compiler"])
+@pytest.mark.parametrize("current", [True, False])
+def test_build_goes_on_without_it(module, monkeypatch, tmp_path, why, current):
+    if why == "no nvcc":
+        monkeypatch.setattr(build, "_nvcc", no_nvcc)
+    elif why == "no headers":
+        monkeypatch.setattr(build.sysconfig, "get_path", lambda name: str(tmp_path))
+    else:
+        monkeypatch.setenv("CXX", str(tmp_path / "none"))
+    if not current:
+        older(module)
+    assert build.build() == build.LIB_PATH
+    # a module of older sources would call the library by an older header
+    assert module.exists() == current
+
+
+def test_the_module_is_there_while_the_next_is_built(module, monkeypatch):
+    seen = []
+
+    def run(cmd, verbose):
+        seen.append(module.read_bytes())
+        open(cmd[cmd.index("-o") + 1], "wb").write(b"after")
+
+    monkeypatch.setattr(build, "_run", run)
+    build.build()
+    assert seen == [b"before"] and module.read_bytes() == b"after"
+    assert not build._torch_stale()
