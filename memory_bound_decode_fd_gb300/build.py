@@ -92,7 +92,7 @@ def _build_torch(verbose: bool) -> None:
     import torch
 
     root = Path(torch.__file__).parent
-    tmp = TORCH_PATH.with_suffix(".so.tmp")
+    tmp = TORCH_PATH.with_name(f"_fd_torch.{os.getpid()}.tmp.so")  # of this process: others may build too
     try:
         cuda = Path(_nvcc()).resolve().parent.parent
         _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
@@ -101,6 +101,7 @@ def _build_torch(verbose: bool) -> None:
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", str(TORCH_SRC), "-o", str(tmp),
               f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], verbose)
     except (RuntimeError, OSError) as e:
+        tmp.unlink(missing_ok=True)
         print(f"_fd_torch.so not built, attention.py's calls stay in Python: {e}", file=sys.stderr)
         return leave_out()
     os.replace(tmp, TORCH_PATH)

@@ -54,3 +54,24 @@ def test_the_module_is_there_while_the_next_is_built(module, monkeypatch):
     build.build()
     assert seen == [b"before"] and module.read_bytes() == b"after"
     assert not build._torch_stale()
+
+
+def test_processes_that_build_at_once_do_not_share_a_file(module, monkeypatch):
+    names = []
+
+    def run(cmd, verbose):
+        out = cmd[cmd.index("-o") + 1]
+        names.append(out)
+        assert not os.path.exists(out)
+        open(out, "wb").write(b"half")
+        if len(names) == 1:  # another process builds meanwhile, and fails
+            monkeypatch.setattr(build.os, "getpid", lambda: 1)
+            build._build_torch(False)
+            assert not os.path.exists(names[1])
+            open(out, "ab").write(b"whole")
+        else:
+            raise RuntimeError("killed")
+
+    monkeypatch.setattr(build, "_run", run)
+    build._build_torch(False)
+    assert names[0] != names[1] and module.read_bytes() == b"halfwhole"
