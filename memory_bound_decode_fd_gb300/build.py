@@ -72,19 +72,31 @@ def _torch_older(path: Path) -> bool:
     return any(p.stat().st_mtime > made for p in (TORCH_SRC, INCLUDE / "fd.h"))
 
 
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def _not_built() -> str:
+    """What TORCH_STAMP holds where ``_fd_torch.so`` does not compile."""
+    return f"{_torch_version()} not built with {_cxx()}"
+
+
 def _torch_stale() -> bool:
-    if not TORCH_PATH.exists() or not TORCH_STAMP.exists() or TORCH_STAMP.read_text() != _torch_version():
-        return True
-    return _torch_older(TORCH_PATH)
+    stamp = TORCH_STAMP.read_text() if TORCH_STAMP.exists() else None
+    if stamp == _not_built():
+        return _torch_older(TORCH_STAMP)
+    return stamp != _torch_version() or not TORCH_PATH.exists() or _torch_older(TORCH_PATH)
 
 
 def _build_torch(verbose: bool) -> None:
     """``_fd_torch.so``. Where it cannot be built, one from before is left if it is of the present
     sources (that it is of another torch is found when it is loaded), else removed."""
 
-    def leave_out() -> None:
+    def leave_out(why: Exception | None = None) -> None:
         if TORCH_PATH.exists() and _torch_older(TORCH_PATH):
             TORCH_PATH.unlink(missing_ok=True)
+        if why:
+            print(f"_fd_torch.so not built, attention.py's calls stay in Python: {why}", file=sys.stderr)
 
     version, python = _torch_version(), sysconfig.get_path("include")
     if version is None or not Path(python, "Python.h").exists():
@@ -95,15 +107,19 @@ def _build_torch(verbose: bool) -> None:
     tmp = TORCH_PATH.with_name(f"_fd_torch.{os.getpid()}.tmp.so")  # of this process: others may build too
     try:
         cuda = Path(_nvcc()).resolve().parent.parent
-        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
+    except RuntimeError as e:
+        return leave_out(e)
+    try:
+        _run([_cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
               f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}", f"-I{python}",
               f"-I{cuda / 'include'}", f'-DFD_TORCH_VERSION="{torch.__version__}"',
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", str(TORCH_SRC), "-o", str(tmp),
               f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], verbose)
     except (RuntimeError, OSError) as e:
         tmp.unlink(missing_ok=True)
-        print(f"_fd_torch.so not built, attention.py's calls stay in Python: {e}", file=sys.stderr)
-        return leave_out()
+        if isinstance(e, RuntimeError):  # it does not compile: not tried again until something is new
+            TORCH_STAMP.write_text(_not_built())
+        return leave_out(e)
     os.replace(tmp, TORCH_PATH)
     TORCH_STAMP.write_text(version)
 

@@ -75,3 +75,29 @@ def test_processes_that_build_at_once_do_not_share_a_file(module, monkeypatch):
     monkeypatch.setattr(build, "_run", run)
     build._build_torch(False)
     assert names[0] != names[1] and module.read_bytes() == b"halfwhole"
+
+
+def test_what_does_not_compile_is_not_tried_again(module, monkeypatch, tmp_path):
+    runs = []
+
+    def run(cmd, verbose):
+        runs.append(cmd)
+        raise RuntimeError("does not compile")
+
+    monkeypatch.setattr(build, "_run", run)
+    for _ in range(3):
+        build.build()
+    assert len(runs) == 1
+    monkeypatch.setenv("CXX", "another")  # until there is another compiler,
+    build.build()
+    build.build()
+    assert len(runs) == 2
+    older(build.TORCH_STAMP)  # or another source
+    build.build()
+    build.build()
+    assert len(runs) == 3
+    # what is merely missing is looked for every time
+    build.TORCH_STAMP.unlink()
+    monkeypatch.setattr(build, "_nvcc", no_nvcc)
+    build.build()
+    assert build._torch_stale()
