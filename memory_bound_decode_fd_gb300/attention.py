@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import sys
 
 import torch
 
@@ -24,7 +25,7 @@ _HEADS = struct.Struct("=Qqqi4x")
 _CACHE = struct.Struct("=QQqqqqqqiiii")
 _BATCH = struct.Struct("=QQQiiiii4x")
 
-_fast = None  # csrc/fd_torch.cpp, from the first call on (False: not built, or against another torch)
+_fast = None  # csrc/fd_torch.cpp, from the first call on (False: not built, or for another torch or Python)
 
 
 def _load():
@@ -37,9 +38,13 @@ def _load():
         except ImportError:
             _fast = False
         else:
-            _fd_torch.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                             for f in (lib.fd_rope, lib.fd_rope_append, lib.fd_paged_attention)))
-            _fast = _fd_torch if _fd_torch.torch_version == torch.__version__ else False
+            python = getattr(_fd_torch, "python_version", None)
+            if _fd_torch.torch_version == torch.__version__ and python == "%d.%d" % sys.version_info[:2]:
+                _fd_torch.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                                 for f in (lib.fd_rope, lib.fd_rope_append, lib.fd_paged_attention)))
+                _fast = _fd_torch
+            else:
+                _fast = False
     return lib
 
 

@@ -263,9 +263,16 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fd_torch", nullptr, -1, methods, 
 
 }  // namespace
 
-// `torch_version`: whose headers this was built against (its classes are used as they lie in memory).
+#define FD_TEXT_OF(x) #x
+#define FD_TEXT(x) FD_TEXT_OF(x)
+
+// `torch_version`, `python_version`: whose headers this was built against (their objects are used as they
+// lie in memory).
 PyMODINIT_FUNC PyInit__fd_torch() {
     PyObject *m = PyModule_Create(&module);
-    if (m && PyModule_AddStringConstant(m, "torch_version", FD_TORCH_VERSION) < 0) Py_CLEAR(m);
+    if (m && (PyModule_AddStringConstant(m, "torch_version", FD_TORCH_VERSION) < 0 ||
+              PyModule_AddStringConstant(m, "python_version",
+                                         FD_TEXT(PY_MAJOR_VERSION) "." FD_TEXT(PY_MINOR_VERSION)) < 0))
+        Py_CLEAR(m);
     return m;
 }

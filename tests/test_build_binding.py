@@ -2,10 +2,14 @@
 processes: the library's build never fails for it, and a good module is never lost."""
 
 import os
+import sys
+import types
 
 import pytest
+import torch
 
-from memory_bound_decode_fd_gb300 import build
+import memory_bound_decode_fd_gb300 as package
+from memory_bound_decode_fd_gb300 import attention, build
 
 
 @pytest.fixture
@@ -101,3 +105,26 @@ def test_what_does_not_compile_is_not_tried_again(module, monkeypatch, tmp_path)
     monkeypatch.setattr(build, "_nvcc", no_nvcc)
     build.build()
     assert build._torch_stale()
+
+
+@pytest.mark.parametrize("torch_version,python_version,used", [
+    (None, None, True), ("1.0", None, False), (None, "2.7", False), ("1.0", "2.7", False)])
+def test_a_module_for_another_python_or_torch_is_not_used(fdlib, monkeypatch, torch_version, python_version, used):
+    module = types.ModuleType("_fd_torch")
+    module.torch_version = torch_version or torch.__version__
+    module.python_version = python_version or f"{sys.version_info.major}.{sys.version_info.minor}"
+    calls = []
+    module.init = lambda *addresses: calls.append(addresses)
+    monkeypatch.setattr(package, "_fd_torch", module, raising=False)
+    monkeypatch.setitem(sys.modules, package.__name__ + "._fd_torch", module)
+    monkeypatch.setattr(attention, "_fast", None)
+    attention._load()
+    assert attention._fast is (module if used else False)
+    assert len(calls) == used  # nothing of it is called before it is known to fit
+
+
+def test_the_module_names_the_python_it_is_for(fdlib):
+    attention._load()
+    if not attention._fast:
+        pytest.skip("not built")
+    assert attention._fast.python_version == f"{sys.version_info.major}.{sys.version_info.minor}"
