@@ -555,7 +555,7 @@ int fd_rope(const fd_heads *q, const fd_heads *k, const fd_heads *q_out, const f
  * is above max_pages * page_size nothing is written, and FD_DEVICE_STATUS_BAD_PAGE is set. max_q
  * is not used. Two sequences must not
  * write the same place of a shared page in one call. The cache may not overlap itself, q, k, v or
- * q_out.
+ * q_out, and neither it nor q_out the positions, inv_freq or the batch's arrays (FD_ERR_OVERLAP).
  */
 int fd_rope_append(const fd_heads *q, const fd_heads *k, const fd_heads *v, const fd_heads *q_out,
                    const fd_paged_cache *cache, const fd_paged_batch *batch, const int *positions,

@@ -156,6 +156,12 @@ int check_batch(const fd_paged_batch &b, int page_size) {
     return FD_OK;
 }
 
+// Whether memory that a call writes is part of the batch's index arrays.
+bool meets_index(const Span &out, const fd_paged_batch &b) {
+    return span_meets(out, b.q_start, 4ll * (b.batch + 1)) || span_meets(out, b.kv_len, 4ll * b.batch) ||
+           (b.max_pages > 0 && span_meets(out, b.block_table, 4ll * ((long long)(b.batch - 1) * b.table_stride + b.max_pages)));
+}
+
 HeadsView view(const fd_heads &h) {
     return {static_cast<uint16_t *>(h.data), h.token_stride, h.head_stride};
 }
@@ -285,6 +291,11 @@ int fd_rope_append(const fd_heads *q, const fd_heads *k, const fd_heads *v, cons
         if (span_meets(s, cache->k, kb) || span_meets(s, cache->v, vb)) return FD_ERR_OVERLAP;
     }
     if (span_meets(o, cache->k, kb) || span_meets(o, cache->v, vb)) return FD_ERR_OVERLAP;
+    for (const Span &w : {o, Span{reinterpret_cast<uintptr_t>(cache->k), kb, 0, 0},
+                          Span{reinterpret_cast<uintptr_t>(cache->v), vb, 0, 0}})
+        if (meets_index(w, *batch) || span_meets(w, inv_freq, 4ll * rot_dim) ||
+            (positions && span_meets(w, positions, 4ll * n)))
+            return FD_ERR_OVERLAP;
     if (!keys_apart(*cache, dk, dv, kb, vb)) return FD_ERR_OVERLAP;
     if (api_launch_fails()) return api_status(cudaErrorLaunchOutOfResources);
     RopeArgs a{};
