@@ -572,7 +572,8 @@ int fd_rope_append(const fd_heads *q, const fd_heads *k, const fd_heads *v, cons
  *   lse_i    = ln sum_j exp(s(i, j))
  * Query head h reads key head h / (q_heads / kv_heads). A row that sees no key (kv_len 0, or
  * fewer keys than new tokens) gives zeros and lse = -infinity.
- * q, out    [total_q] tokens of q heads; out must not overlap q or the cache.
+ * q, out    [total_q] tokens of q heads. out, lse and scratch must not overlap one another, q, the
+ *           cache or the batch's arrays (FD_ERR_OVERLAP).
  * lse       fp32 [total_q, q_heads], 4-byte aligned, or NULL.
  * scratch   device memory of at least fd_paged_attention_scratch_bytes(...) bytes, 16-byte
  *           aligned, ZERO before its first use; every completed call leaves its counters zero

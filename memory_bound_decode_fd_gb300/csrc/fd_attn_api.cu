@@ -353,10 +353,11 @@ int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_
         return FD_ERR_OVERLAP;
     const Span sc{reinterpret_cast<uintptr_t>(scratch), (long long)need, 0, 0};
     if (span_meets(sc, cache->k, kb) || span_meets(sc, cache->v, vb)) return FD_ERR_OVERLAP;
+    if (meets_index(o, *batch) || meets_index(sc, *batch)) return FD_ERR_OVERLAP;
     if (lse) {
         const Span ls{reinterpret_cast<uintptr_t>(lse), lse_bytes, 0, 0};
         if (span_meets(o, lse, lse_bytes) || span_meets(i, lse, lse_bytes) || span_meets(sc, lse, lse_bytes) ||
-            span_meets(ls, cache->k, kb) || span_meets(ls, cache->v, vb))
+            span_meets(ls, cache->k, kb) || span_meets(ls, cache->v, vb) || meets_index(ls, *batch))
             return FD_ERR_OVERLAP;
     }
     if (api_launch_fails()) return api_status(cudaErrorLaunchOutOfResources);

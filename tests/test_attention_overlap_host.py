@@ -28,3 +28,19 @@ TABLE = (3 * 10 + 10) * 4                            # of the block table, batch
 ])
 def test_append_over_its_index(no_launch, kw, status):  # noqa: F811
     assert append(no_launch, **kw) == status
+
+
+LSE = 8 * 32 * 4
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(b=batch(q_start=O + 64)), OVER), (dict(b=batch(kv_len=O + 64)), OVER), (dict(b=batch(table=O + 64)), OVER),
+    (dict(b=batch(q_start=S + 64)), OVER), (dict(b=batch(kv_len=S + 64)), OVER), (dict(b=batch(table=S + 64)), OVER),
+    (dict(lse=QS), OVER), (dict(lse=KL), OVER), (dict(lse=BT), OVER),
+    (dict(lse=QS - LSE), RUNS), (dict(lse=QS - LSE + 4), OVER), (dict(lse=QS + 20), RUNS), (dict(lse=QS + 16), OVER),
+    (dict(lse=KL + 16), RUNS), (dict(lse=KL + 12), OVER), (dict(lse=BT + TABLE), RUNS), (dict(lse=BT + TABLE - 4), OVER),
+    (dict(b=batch(table=O, max_pages=0)), RUNS),
+    (dict(b=batch(q_start=KC), c=cache()), RUNS),    # what is only read may be anywhere
+])
+def test_attention_over_its_index(no_launch, kw, status):  # noqa: F811
+    assert attend(no_launch, **kw) == status
