@@ -308,6 +308,8 @@ def paged_attention(
         raise ValueError(f"q has {h} heads: not a multiple of the cache's {hk}")
     if max_q < 0 or window < 0:
         raise ValueError("max_q and window must not be negative")
+    if softcap and not ctypes.c_float(softcap).value:
+        raise ValueError(f"softcap {softcap} is 0, which means none, in 32 bits")
     batch = _batch(q_start, kv_len, block_table, dev, n, min(max_q, n))
     work = _flat("scratch", scratch, dev, torch.uint8)
     if out is None:

@@ -202,7 +202,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     int64_t max_q = 0, window = 0, bytes = 0;
     const int causal = n_args == 14 ? truth(a[9]) : -1;
     if (causal < 0 || !whole(a[6], &max_q) || !whole(a[10], &window) || !number(a[11], &softcap) ||
-        (a[8] != Py_None && !number(a[8], &scale)) || max_q < 0 || window < 0)
+        (a[8] != Py_None && !number(a[8], &scale)) || max_q < 0 || window < 0 || (softcap != 0 && (float)softcap == 0))
         Py_RETURN_NONE;
     Call c;
     fd_heads qh{}, oh{};

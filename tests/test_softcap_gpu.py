@@ -13,6 +13,7 @@ import torch
 
 import memory_bound_decode_fd_gb300 as fd
 from attn_check import U16, U32, Batch
+from memory_bound_decode_fd_gb300 import attention
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +89,15 @@ def test_small_scores_beside_ones_past_the_cap(cuda_device, q_lens, kv_lens, d):
 def test_scale_far_below_the_cap(cuda_device, q_lens, kv_lens, d):
     # scale / cap is no 32-bit number, the scores are ordinary
     check(Batch(8, 2, d, q_lens, kv_lens, 16, seed=45, q_std=2.0**60), 1e30, 2.0**-60 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("fast", [True, False])
+@pytest.mark.parametrize("cap", [1e-46, -1e-46, 5e-324])
+def test_a_cap_that_32_bits_take_for_none_is_refused(cuda_device, monkeypatch, cap, fast):
+    attention._load()
+    if not fast:
+        monkeypatch.setattr(attention, "_fast", False)
+    b = Batch(4, 2, 64, [1, 1], [20, 30])
+    scratch = fd.paged_attention_scratch(2, 2, 4, 2, 64, 1)
+    with pytest.raises(ValueError, match="softcap"):
+        fd.paged_attention(b.q, *b.args(), 1, scratch, softcap=cap)
