@@ -599,7 +599,8 @@ int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_
 
 /* Bytes of scratch that suffice for every fd_paged_attention call with these heads and head_dim
  * whose batch, total_q and max_q are at most these (host only; 0 for a size that the call refuses):
- * 4 MB at most for single tokens, 67 MB where max_q * q_heads / kv_heads > 16. */
+ * 4.3 MB at most where max_q * q_heads / kv_heads is up to 16 (or more than 128 heads share a key head),
+ * 68.2 MB at most where it is more. */
 size_t fd_paged_attention_scratch_bytes(int batch, int total_q, int q_heads, int kv_heads,
                                         int head_dim, int max_q);
 
