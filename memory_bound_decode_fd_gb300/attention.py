@@ -83,8 +83,12 @@ def _heads(name: str, t: _Tensor, dev: int, n=None, h=None, d=None) -> bytes:
     raise _refuse(name, t, _BF16, (n, h, d), "[tokens, heads, head_dim]")
 
 
-def _new(like: _Tensor, shape: torch.Size) -> tuple[_Tensor, bytes]:
-    """A new contiguous bf16 [tokens, heads, head_dim] tensor beside `like`, and its fd_heads."""
+def _new(like: _Tensor, shape: torch.Size, stream) -> tuple[_Tensor, bytes]:
+    """A new contiguous bf16 [tokens, heads, head_dim] tensor beside `like`, of the stream that the call
+    is made on, and its fd_heads."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _new(like, shape, None)
     # (the likeness of a dense tensor is the cheaper call)
     t = torch.empty_like(like) if like.is_contiguous() else torch.empty(shape, dtype=_BF16, device=like.device)
     n, h, d = shape
@@ -189,13 +193,13 @@ def rope(
     if k is not None:
         kb = _heads("k", k, dev, n, None, d)
         if k_out is None:
-            k_out, ko = _new(k, k.shape)
+            k_out, ko = _new(k, k.shape, stream)
         else:
             ko = _heads("k_out", k_out, dev, *k.shape)
     elif k_out is not None:
         raise ValueError("k_out without k")
     if q_out is None:
-        q_out, qo = _new(q, shape)
+        q_out, qo = _new(q, shape, stream)
     else:
         qo = _heads("q_out", q_out, dev, *shape)
     _call(dev, lib.fd_rope, qb, kb, qo, ko, pos, freq, n, d, rot, 1 if interleaved else 0, scale,
@@ -246,7 +250,7 @@ def rope_append(
     batch = _batch(q_start, kv_len, block_table, dev, n, n)
     pos = None if positions is None else _flat("positions", positions, dev, _I32, n)
     if q_out is None:
-        q_out, qo = _new(q, shape)
+        q_out, qo = _new(q, shape, stream)
     else:
         qo = _heads("q_out", q_out, dev, *shape)
     _call(dev, lib.fd_rope_append, qb, kb, vb, qo, cache, batch, pos, freq, rot,
@@ -313,7 +317,7 @@ def paged_attention(
     batch = _batch(q_start, kv_len, block_table, dev, n, min(max_q, n))
     work = _flat("scratch", scratch, dev, torch.uint8)
     if out is None:
-        out, ob = _new(q, shape)
+        out, ob = _new(q, shape, stream)
     else:
         ob = _heads("out", out, dev, *shape)
     lse_ptr = None
