@@ -147,7 +147,9 @@ cudaError_t status_attn_tc(cudaStream_t stream, unsigned *out, bool clear);
 // Which of the two: up to 16 rows a key head are one pass of the first (16 sequences of up to 6000,
 // 4 heads a key head: 4 new tokens, 16 rows, 51 us in the first and 65 in the second; 8, 32 rows, 78
 // in two passes of the first and 51 in the second); a group of more than 128 query heads does not
-// fit the second's tile, and it wants a positive scale.
+// fit the second's tile, and it wants a positive scale. The batch's longest chunk decides for all of it:
+// 32 tokens and a chunk of 512, 8192 keys each, take 235 us in one call, 162 and 61 in two. 64 single tokens
+// of 4096 keys take 38 us with 32 heads on one (the second kernel), 33 with 16 on one.
 inline bool attn_uses_tc(int max_q, int group, float scale) {
     return (long long)max_q * group > kRowsM && group <= kAttnTcTile && scale > 0.f;
 }

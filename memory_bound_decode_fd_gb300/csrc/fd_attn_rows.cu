@@ -6,7 +6,7 @@
 // 16 multiply-adds per byte of the cache, far below what the tensor cores do, so what matters is
 // that every SM streams pages all the time.
 //
-//   * The keys of all (sequence, block of 16 rows, key head) items, in tiles of 16 keys a warp,
+//   * The keys of all (sequence, block of 16 rows, key head) items, in tiles of 32 keys a warp,
 //     form one long list, and CTA c of G takes tiles [T c / G, T (c + 1) / G) of it: every SM gets
 //     the same number of tiles whatever the lengths of the sequences, with nothing planned on the
 //     host (the lengths are device memory, a captured graph sees new ones). An item that several
@@ -14,8 +14,8 @@
 //     accumulator) to its own slot, takes a ticket, and the holder of the last ticket adds the
 //     slots in the order of the CTAs, so results do not depend on who is last. Where whole items
 //     are dealt out evenly enough, no item is shared (kJoinTiles): 128 sequences of up to 1000 at
-//     head_dim 64 take 37 us in whole items, 47 in shared ones, 64 of up to 8192 at 128 take 239
-//     and 185.
+//     head_dim 64 take 36 us in whole items, 47 in shared ones, 64 of up to 8192 at 128 take 239
+//     and 186.
 //   * Each of the warps that compute has a warp that copies for it: its 32 keys and values of a
 //     tile, by tensor-map copies (64 elements of the tokens of a page, 128-byte swizzle) into a
 //     ring of their own in shared memory, across the ends of items; page numbers are read kAhead

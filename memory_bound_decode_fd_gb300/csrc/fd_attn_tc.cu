@@ -6,8 +6,10 @@
 // values, copied once, serves all the heads that share it. Per tile of 128 keys and half:
 //     S = Q K^T (128 x 128 in tensor memory),  P = exp(S - m),  O = O + P V (in tensor memory).
 // Bound by the tensor cores: 4 * 128 * 128 * D flops a tile and half. A prompt of 8192 (32 heads on
-// 8, D 128) takes 363 us: 1515 TFLOP/s, 79 % of what a large matrix product reaches; 512 tokens
-// behind 16000 118 us, 1150 TFLOP/s. A CTA spends 3500 cycles on a tile of both halves: the 32
+// 8, D 128) takes 361 us: 1520 TFLOP/s, 79 % of what a large matrix product reaches, while the SM clock
+// is 2070 MHz. Run on end for longer than some 50 ms, singly or in a graph, it takes 382 (1440 TFLOP/s,
+// 85 % of the product's rate under the power limit): the clock is then 1960 MHz. 512 tokens behind 16000
+// take 118 us, 1150 TFLOP/s. A CTA spends 3500 cycles on a tile of both halves: the 32
 // MMAs take 70 each, 2250 in all (64 at the tensor cores' full rate), and for the rest the tensor
 // cores wait for probabilities, a half's softmax (1600 cycles, latencies more than issue slots) being
 // longer than the other half's MMAs (1130). At D = 64 the MMAs are shorter and the softmax is not:
@@ -19,6 +21,7 @@
 //     softmax of one half each, two threads a row. While one half is in the softmax the tensor cores
 //     run the other's P V and next S: per tile the MMA warp issues, for each half in turn, P V of
 //     this tile and then S of the next, and never waits for its own results.
+//   * Registers: at 104 a softmax thread the kernels spill 8 to 14 words a thread, with large caps 17.
 //   * S, P and O stay in tensor memory: P (bf16, two a column) takes the first half of S's
 //     columns and is the A operand of the second product from there. MMAs run in the order of
 //     issue, so the next S may overwrite P without a wait. Q and both operands of S are
@@ -963,8 +966,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the items that several CTAs of a list had a part of, in the order of the CTAs: block (c, y)
 // the rows 32 y .. of the item that begins in CTA c. By itself and over the whole GPU: a part is
-// up to 128 KB, and joined by the last CTA to finish, six of them took 14 us. Its blocks are in
-// place before the parts are written, and wait for them.
+// up to 128 KB, and joined by the last CTA to finish, six of them took 14 us. The programmatic launch
+// hides the launch alone: an attention CTA holds 61440 of its SM's 65536 registers, so a block of this
+// kernel starts where one of those has ended.
 constexpr int kJoinRows = 32, kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_tc_join_kernel(const AttnArgs a, int tokens) {
