@@ -602,8 +602,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         int x = deal.begin;
+        // Over codes, runs without a tile come after the others: a warp that converts holds a tile while it looks for the next,
+        // and a place in the ring is free only when the softmax has had the run's tiles, so that each would wait for the other
+        // where more such runs than the ring holds lay in between.
+        bool tiles = true, skipped = false;
         for (int n = 0;; ++n) {
             Segment g{};
+            if (KV8 && x >= deal.end && tiles && skipped) x = deal.begin, tiles = false;
             if (x < deal.end) {
                 g.valid = 1;
                 int from = 0, to = 1 << 30, t;
@@ -642,6 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int base = deal.run == 0 ? 0 : pair_tiles<SINKS>(g.s, a, g.i0, tokens).a;
                 clip_halves<SINKS>(g, a, tokens, base + from, base + to);
                 x = g.next;
+                if (KV8 && (g.jb > g.ja) != tiles) {
+                    skipped = true, --n;
+                    continue;
+                }
             }
             // room for it (bounded: those who hold a run give up on their own waits)
             const long long t0 = clock64();
@@ -676,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++j;
             while (more && j >= jb) {
                 const volatile Segment &g = take(n);
-                more = g.valid;
+                more = g.valid && g.jb > g.ja;  // (behind the first run without a tile there is none)
                 if (!more) break;
                 hk = g.hk, j = g.ja, jb = g.jb, lo = g.lo, hi = g.hi, shift = g.shift;
                 row = a.m.table + (long long)g.b * a.m.table_stride;
@@ -759,9 +768,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) load(1);
             ++tiles;
         }
-        for (; more; ++n) {  // a wait gave up: the others count on every run's release
-            more = take(n).valid;
-            if (more) release(n);
+        for (bool rest = true; rest; ++n) {  // runs without tiles, or a wait gave up: the others count on every run's release
+            rest = take(n).valid;
+            if (rest) release(n);
         }
     } else {
         // --------------------------------------------------------- softmax, a thread a row
