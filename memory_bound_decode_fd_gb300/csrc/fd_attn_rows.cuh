@@ -623,7 +623,8 @@ __global__ void __launch_bounds__(RowsShape<D, TYPE != 0, ROWS>::kThreads, 1)
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
                 // Row 8 r + g8, elements 2 c2 .. + 3 of each 16, as a lane gets them of the keys. In f16, the row's largest
-                // between 2^13 and 2^14: exact for all that are no smaller than 2^-27 of it, the others off by 2^-39 of it.
+                // between 2^14 and 2^15: exact for all that are no smaller than 2^-31 of it, the others off by half of fp16's smallest
+                // step, 2^-25, or 2^-39 of it. (Below 2^-100 nothing is lost: bf16's own smallest step is 2^-19 there.)
                 const int all = g.rb * S::kRows + 8 * r + g8, i = all / a.group;
                 const bool live = 8 * r + g8 < g.rows;
                 const uint16_t *q = a.q.p + (g.s.q0 + i) * a.q.ts + (g.hk * a.group + all - i * a.group) * a.q.hs + 2 * c2;
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(RowsShape<D, TYPE != 0, ROWS>::kThreads, 1)
                 }
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                const int k = max((int)(top >> 23) - 127, -100) - 13;
+                const int k = max((int)(top >> 23) - 127, -100) - 14;
                 const float f = two_to(-k), mul = (CAPPED ? 1.f : to_log2) * two_to(k);
 #pragma unroll
                 for (int ks = 0; ks < kC; ++ks)
