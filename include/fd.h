@@ -529,7 +529,8 @@ typedef struct fd_paged_batch {
  * k_scale, v_scale  bytes (E8M0: a biased exponent). That of (page, block, head), block = token of the page /
  *          FD_KV8_BLOCK, is k_scale[page * k_scale_page_stride + block * k_scale_block_stride +
  *          head * k_scale_head_stride]. Strides not negative, any alignment.
- * Half the bytes of fd_paged_cache. A code's value is exact in bf16.
+ * Half the bytes of fd_paged_cache. A code's value is exact in bf16 where its scale byte is 3 .. 246 (int8: 1 .. 247), as
+ * those of all tokens that are seen have to be.
  */
 typedef struct fd_paged_cache_kv8 {
     void *k;
@@ -605,11 +606,12 @@ int fd_rope_append(const fd_heads *q, const fd_heads *k, const fd_heads *v, cons
  *   e        = e_new where the block's first token is new; else max(e_new, e before), and where that is
  *              more than before, the block's earlier codes become round(code * 2^(e before - e))
  *   code     = round(x * 2^-e);  scale byte = e + 127
- * round: to the nearest code, ties to the even one. x is the rotated key, or the value, in 32 bits: rounded once. A
+ * round: to the nearest code, ties to the even one. x is the rotated key, or the value, in 32 bits: rounded once. (A key's
+ * cosines and sines have fd_rope's error: next to the border of two codes, or of two scales, it may take either.) A
  * prompt and the same tokens one by one need not leave the same codes. What a block holds behind its
  * new tokens is left as it is.
- * Keys and values should be finite. An infinity is held as the largest code of its sign and a NaN as NaN
- * (E4M3) or 0 (int8); e is then that of the finite ones.
+ * Keys and values should be below 2^126 in size (larger ones may have a code whose value is past bf16's range). An
+ * infinity is held as the largest code of its sign and a NaN as NaN (E4M3) or 0 (int8); e is then that of the finite ones.
  * Two sequences must not write to the same block of a shared page in one call. Scales must each have a place
  * of their own; neither they nor the codes may overlap one another, the activations, positions,
  * inv_freq or the batch's arrays (FD_ERR_OVERLAP). All else is as in fd_rope_append: the rotation, tokens
@@ -659,7 +661,8 @@ int fd_paged_attention(const fd_heads *q, const fd_paged_cache *cache, const fd_
  * fd_paged_attention_sinks - fd_paged_attention with a window beside which the first `sinks` tokens of
  * each sequence stay visible (attention sinks): a row sees j < sinks and j > p_i - window, of those
  * that it sees without a window. Pages between the sinks and the window are not read, and their
- * entries of the block table neither.
+ * entries of the block table neither. Keys lie rotated in the cache, so a sink is seen at its own distance: a model
+ * whose sinks are to be moved next to the window, for sequences longer than it was trained on, is not run so.
  * Requires  sinks >= 0; without a window (0) sinks change nothing.
  */
 int fd_paged_attention_sinks(const fd_heads *q, const fd_paged_cache *cache, const fd_paged_batch *batch,
@@ -682,7 +685,8 @@ int fd_paged_attention_kv8(const fd_heads *q, const fd_paged_cache_kv8 *cache, c
 /* Bytes of scratch that suffice for every fd_paged_attention (_sinks, _kv8) call with these heads and head_dim
  * whose batch, total_q and max_q are at most these (host only; 0 for a size that the call refuses):
  * 4.3 MB at most where max_q * q_heads / kv_heads is up to 16 (or more than 128 heads share a key head),
- * 68.2 MB at most where it is more. */
+ * 68.2 MB at most where it is more. The kind of cache does not enter: over 8 bits 17 to 32 rows use the smaller one's part
+ * of it and are asked for the larger all the same. */
 size_t fd_paged_attention_scratch_bytes(int batch, int total_q, int q_heads, int kv_heads,
                                         int head_dim, int max_q);
 

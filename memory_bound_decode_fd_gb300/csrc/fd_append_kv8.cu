@@ -14,7 +14,8 @@
 // quarters of the bytes, are in bf16 as they come) and by latency for single tokens (one: 4.5 to 5 us, 64: 5.5, the
 // launch and three dependent loads). In the prompts every unit waits for its block's angles and its rows, and the
 // rotation is done twice, for the maximum and for the codes: rows held in 32 bits between the two took 42 us, with
-// twice the registers and half the warps. A CTA takes the blocks that begin in a
+// twice the registers and half the warps. Angles are those of fd_rope, their cosines and sines in 32 bits (off by a few
+// 2^-24): an element next to the border of two codes may so take either, and a maximum next to that of two scales too. A CTA takes the blocks that begin in a
 // run of `run` tokens (a block begins at a sequence's first new token or at a multiple of 16): its threads look
 // up all tokens of the run, make the cosines and sines of a block's tokens in shared memory, then its
 // warps take heads of keys and values, and its threads units of 16 elements of the queries.
@@ -340,7 +341,10 @@ cudaError_t launch_d(const RopeArgs &a, const Kv8Cache &c, cudaStream_t stream) 
     cudaError_t err = device_info(&di);
     if (err != cudaSuccess) return err;
     const bool vec = a.rot_dim % kUnit == 0;
-    // few tokens: one a CTA, its heads over several, a warp's worth of them each
+    // Up to four tokens an SM: one a CTA, and up to one an SM its heads over several CTAs. Of a sequence's tokens
+    // only the first of each block then finds work, so that this suits single tokens (64: 5.1 us, 16 a CTA 40; 608: 14
+    // and 43) and not chunks (one of 512: 15.4 us, 16 a CTA 8.0). Above, CTAs of 16 tokens suit chunks (one of 1200: 8.4 us,
+    // one a CTA 18) and not single tokens, up to 16 blocks one after the other in a CTA (1024: 43 us, one a CTA 23).
     const bool few = a.tokens <= 4 * di.sm_count;
     const int run = few ? 1 : kMostRun;
     const int jobs = 2 * a.k_heads + (a.q_heads * D + 511) / 512;

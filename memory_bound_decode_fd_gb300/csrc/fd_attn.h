@@ -181,9 +181,9 @@ cudaError_t status_attn_tc_kv8(cudaStream_t stream, unsigned *out, bool clear);
 // fit the second's tile, and it wants a positive scale. The batch's longest chunk decides for all of it:
 // 32 tokens and a chunk of 512, 8192 keys each, take 235 us in one call, 162 and 61 in two. 64 single tokens
 // of 4096 keys take 38 us with 32 heads on one (the second kernel), 33 with 16 on one.
-// Over a cache in 8 bits two passes of the first kernel are the shorter ones too (16 sequences of 3000, 32 rows:
-// 48 us in the first and 64 in the second, 30 and 49 at head_dim 64; 48 rows 70 and 64; of up to 6000 and 8 to 32 rows
-// 51 and 75).
+// Over a cache in 8 bits two passes of the first kernel are the shorter ones too (16 sequences of 3000, 20 to 32 rows:
+// 49 us in the first and 65 in the second, 31 and 49 at head_dim 64; of up to 6000 and 8 to 32 rows 52 and 76). Three are
+// at head_dim 64 alone (40 to 48 rows: 45 and 49; at 128 74 and 65), four are not (59 and 49, 94 and 65).
 inline bool attn_uses_tc(int max_q, int group, float scale, bool kv8 = false) {
     return (long long)max_q * group > (kv8 ? 2 : 1) * kRowsM && group <= kAttnTcTile && scale > 0.f;
 }

@@ -32,7 +32,7 @@
 //
 // Over a cache in 8 bits (KV8) half of the bytes are to be read, and making operands of the codes costs as much
 // as the copies hide: 64 sequences of up to 8192, 4 heads a key head, take 103 us, 89 % of the copy bandwidth, 2 of
-// 131072 88 us (91 %), one of 4097 10.4. A warp's tile of 32 keys at head_dim 128 is 1750 cycles of work, 500 of
+// 131072 88 to 92 us (88 to 91 %), one of 4097 10.4 to 10.8. A warp's tile of 32 keys at head_dim 128 is 1750 cycles of work, 500 of
 // waiting.
 //   * s(i, j) = 2^ek <q_i, code_j>, and sum_j p_j v_j = sum_j (p_j 2^ev) code_j: the codes go into the MMAs as f16,
 //     exactly and without a scale, the keys' scales are put on the scores and the values' on the probabilities.
@@ -84,7 +84,7 @@ struct RowsShape {
     // some of theirs (0: none do).
     static constexpr int kWorkRegs = KV8 ? 200 : 0, kCopyRegs = 56, kLaunchRegs = 128;
     static_assert(kConsumers * kWorkRegs + (kThreads - kConsumers) * kCopyRegs <= kThreads * kLaunchRegs || !KV8, "registers");
-    // copies of a stage that are counted: one of its rows; of codes also four of scales
+    // arrivals that fill a stage: its rows' copies as one; of codes also a scale for each block of keys and of values
     static constexpr int kArrivals = KV8 ? 1 + 2 * kBlocks : 1;
     static constexpr int kRing = kStages * 2 * kPart;    // of one warp
     static constexpr int kPitch = D + 8;                 // floats; conflict-free accumulator rows
@@ -305,8 +305,9 @@ __global__ void __launch_bounds__(RowsShape<D, TYPE != 0, ROWS>::kThreads, 1)
     {
         const int per = (a.m.batch + kThreads - 1) / kThreads;
         const int b0 = min(tid * per, a.m.batch), b1 = min(b0 + per, a.m.batch);
-        // 16 sequences of 2 to 8 new tokens, 4 heads a key head, up to 6000 keys: 51 us, and 7 more where each counts as two
-        // blocks of 16 rows. For up to 8 blocks, so that the tiles' count stays far from 2^32.
+        // 16 sequences of 2 to 8 new tokens, 4 heads a key head, up to 6000 keys: 52 us, and 60 where each counts as two
+        // blocks of 16 rows; where all have two, 64 of 1000 keys, 77 and 76. For up to 8 blocks, so that the tiles' count
+        // stays far from 2^32.
         deal.ragged = KV8 && row_blocks > 1 && row_blocks <= 8;
         deal.items = row_blocks * a.kv_heads;
         const int G = gridDim.x;

@@ -21,7 +21,7 @@
 //     softmax of one half each, two threads a row. While one half is in the softmax the tensor cores
 //     run the other's P V and next S: per tile the MMA warp issues, for each half in turn, P V of
 //     this tile and then S of the next, and never waits for its own results.
-//   * Registers: at 104 a softmax thread the kernels spill 8 to 14 words a thread, with large caps 17.
+//   * Registers: at 104 a softmax thread the kernels spill 8 to 15 words a thread, with large caps 13 to 20.
 //   * S, P and O stay in tensor memory: P (bf16, two a column) takes the first half of S's
 //     columns and is the A operand of the second product from there. MMAs run in the order of
 //     issue, so the next S may overwrite P without a wait. Q and both operands of S are
@@ -42,16 +42,21 @@
 //     its tensor memory.
 //
 // Over a cache in 8 bits (KV8) the same MMAs run on bf16 operands made of the codes, each times its block's power of
-// two: exact, so results are those of a bf16 cache with these values. (An 8-bit MMA wants probabilities in 8 bits.)
+// two: exact, so the products are those of a bf16 cache with these values; a row's sum is added in another order, and the
+// results differ by that. (An 8-bit MMA wants probabilities in 8 bits.)
 //   * Eight warps convert, 16 rows (one block, one scale) of each tile each: codes by plain loads straight from the
 //     pages, a tile ahead, to the swizzled stages. Eight do the softmax, a thread a row with 136 registers: one
 //     exponential after the other, but no second thread to agree with on the row's maximum.
-//   * A prompt of 8192 takes 548 us (bf16 cache: 361 to 389), 512 tokens behind 16000 158 (118). Both the softmax and the
-//     conversion are chains of 4500 cycles and more a tile, of which the 32 MMAs take 2250. With two threads a row and a
+//   * A prompt of 8192 takes 554 us (bf16 cache: 361 to 389), 512 tokens behind 16000 157 (120). Both the softmax and the
+//     conversion are chains of 4500 cycles and more a tile, of which the 32 MMAs take 2250; 12 words a thread lie
+//     on the stack (stored 35 times, loaded 26), and a warp waits 1.3 cycles for the code of each
+//     instruction: forms of the conversion that differ in a comparison or two take 546 to 590 us. With two threads a row and a
 //     warp each converting keys and values that prompt took 1022 us, with eight converters fed by tensor-map copies
 //     of the codes 575; a third buffer of scores in the softmax spills (588).
 //   * Capped scores are arithmetic of the softmax's warps, of which there are half as many: three prompts of up to
 //     2500 in a window of 512 capped at 30, 28 heads on 4 of 64, 180 us (bf16 cache: 82).
+//   * Runs without a tile come last in a CTA (the dealing warp), or a warp that converts, holding a tile while it looks for
+//     the next one, and the softmax, which that tile is for, could wait for one another.
 #pragma once
 
 #include <algorithm>
